@@ -474,6 +474,106 @@ moe_status_t moe_backward(const moe_layer_desc_t* d, const moe_weights_t* w, con
 /* Number of kernels one moe_backward call with this descriptor launches. */
 int moe_backward_launch_count(const moe_layer_desc_t* d);
 
+/* ---- matrix products grouped by expert ----------------------------------
+ * The products that moe_expert_ffn and moe_backward fuse with their
+ * activations, one by one: for an expert of another form, an optimizer's own
+ * schedule, or a training step that keeps activations (below).  One linear
+ * layer per expert over the dispatch order:
+ *   rows   rows of x, y, dy and dx (an upper bound of offsets[G]);
+ *   offsets device int32 [G + 1], as moe_permute writes it: expert g's rows
+ *          are offsets[g] .. offsets[g+1] (any length, 0 included).  Bounds
+ *          outside [0, rows] are clamped to it and a segment that ends before
+ *          it starts is empty.  Rows behind offsets[G] are not read, and
+ *          their outputs stay as they were;
+ *   w      [G, N, K] in dtype (nn.Linear layout);
+ *   sums   in fp32: on the tensor cores (whose adds truncate) at most 512
+ *          terms at a time when the output is fp32, the parts added in fp32
+ *          with rounding.  Fixed order: the same call gives the same bits.
+ * bf16 runs on the tensor cores when N and K are multiples of 8 (else on the
+ * CUDA cores) and then needs x, dy, w and dw on 16-byte boundaries; fp32 runs
+ * on the CUDA cores.  Tensors must not overlap.  Limits: G <= 1024,
+ * G N K < 2^40, rows, N, K < 2^30.  rows = 0 is valid. */
+
+/* Workspace of moe_grouped_gemm and moe_grouped_dgrad; 0 if an argument is
+ * invalid. */
+size_t moe_grouped_workspace_size(int G, int N, int K, int rows, int dtype);
+
+/* y[r, :] = x[r, :] W_g^T (+ bias[g, :]).  x [rows, K], bias [G, N] or NULL
+ * (dtype), y [rows, N] in out_dtype (MOE_DTYPE_F32, or MOE_DTYPE_BF16 when
+ * dtype is), rounded once. */
+moe_status_t moe_grouped_gemm(const void* x, const void* w, const void* bias, const int32_t* offsets,
+                              int G, int N, int K, int rows, int dtype, int out_dtype, void* y,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* The input gradient: dx[r, :] = dy[r, :] W_g.  dy [rows, N] in dtype, dx
+ * [rows, K] in out_dtype (as moe_grouped_gemm). */
+moe_status_t moe_grouped_dgrad(const void* dy, const void* w, const int32_t* offsets,
+                               int G, int N, int K, int rows, int dtype, int out_dtype, void* dx,
+                               void* ws, size_t ws_bytes, void* stream);
+
+size_t moe_grouped_wgrad_workspace_size(int G, int N, int K, int rows, int dtype);
+
+/* The weight gradient dw[g] = sum over g's rows of dy[r, :]^T x[r, :]
+ * (fp32 [G, N, K]) and, when db is not NULL, the bias gradient db[g] = sum of
+ * dy[r, :] (fp32 [G, N]).  accumulate = 0 overwrites both (an expert without
+ * rows gets zeros); 1 adds onto them (it keeps what it has). */
+moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* offsets,
+                               int G, int N, int K, int rows, int dtype, int accumulate,
+                               float* dw, float* db, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- activation checkpoints in 8 bits ----------------------------------
+ * What a backward needs of the forward, in a byte per value.  A row is cut
+ * into blocks of MOE_CKPT_BLOCK consecutive columns (the last one may be
+ * shorter).  A block keeps e, the exponent field of its largest magnitude as
+ * an fp32 number, and per element
+ *   q = round_to_nearest_even(x 2^(133 - e)), clamped to [-127, 127],
+ * which stands for q 2^(e - 133).  |error| <= 2^(e - 134), 2^(e - 133) at the
+ * clamp: less than 1/64 of the block's largest magnitude.  A block that holds
+ * a NaN or an infinity (e = 255) reads back as NaN throughout.
+ *   q int8 [rows, cols], e uint8 [rows, moe_ckpt_blocks(cols)].
+ * n_rows (device int32, or NULL for all `rows`) limits the rows that are
+ * read and written; the others stay as they were.  Any width; widths that
+ * are a multiple of 8 with every tensor on a 16-byte boundary are the fast
+ * ones. */
+#define MOE_CKPT_BLOCK 32
+
+/* Blocks of a row of `cols` values: ceil(cols / MOE_CKPT_BLOCK). */
+int moe_ckpt_blocks(int cols);
+
+/* Keeps src [rows, cols] (dtype). */
+moe_status_t moe_ckpt_quantize(const void* src, const int32_t* n_rows, int rows, int cols, int dtype,
+                               int8_t* q, uint8_t* e, void* stream);
+
+/* dst[r, :] = the kept row row_index[r] (NULL: r) of src_rows rows, in dtype;
+ * bf16 holds every kept value exactly (subnormals apart).  With row_index =
+ * moe_permute's row_token this reads a layer input back into dispatch order.
+ * An index outside [0, src_rows) gives a zero row and sets
+ * MOE_DEVERR_BAD_ROW_TOKEN in *device_status (a device int32, may be NULL). */
+moe_status_t moe_ckpt_dequantize(const int8_t* q, const uint8_t* e, const int32_t* row_index,
+                                 const int32_t* n_rows, int rows, int src_rows, int cols, int dtype,
+                                 void* dst, int32_t* device_status, void* stream);
+
+/* a = act(h) and the checkpoint of h, in one pass.
+ *   act = MOE_ACT_SWIGLU: h [rows, 2I], gate columns first, a [rows, I] =
+ *     SiLU(gate) * up; q [rows, 2, I] and e [rows, 2, moe_ckpt_blocks(I)]:
+ *     the two halves are cut into blocks apart (as 2 rows rows of I columns);
+ *   act = MOE_ACT_GELU_TANH: h [rows, I], q [rows, I], e [rows, blocks].
+ * h in src_dtype, a in dtype, computed from h in fp32 and rounded once. */
+moe_status_t moe_act_save(const void* h, const int32_t* n_rows, int rows, int I, int act, int dtype,
+                          int src_dtype, void* a, int8_t* q, uint8_t* e, void* stream);
+
+/* The backward of act from the checkpoint (h' = the kept values), in one
+ * pass: with da [rows, I] (src_dtype) the gradient reaching act(h) before the
+ * row's gate weight row_w[r] (fp32, NULL: 1),
+ *   dh = row_w da act'(h')   (dtype, the layout of h)
+ *   wa = row_w act(h')       (dtype [rows, I], may be NULL: the operand of
+ *                             the down projection's weight gradient)
+ *   dw[r] = sum_i da act(h') (fp32 [rows], may be NULL: the gradient
+ *                             reaching row_w). */
+moe_status_t moe_act_backward(const int8_t* q, const uint8_t* e, const void* da, const float* row_w,
+                              const int32_t* n_rows, int rows, int I, int act, int dtype, int src_dtype,
+                              void* dh, void* wa, float* dw, void* stream);
+
 /* ---- diagnostics (no counterpart on the source pages) ------------------- */
 
 /* Self-test of the bounded waits that every pipelined kernel of this library

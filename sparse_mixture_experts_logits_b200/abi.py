@@ -29,7 +29,11 @@ EXPORTED_SYMBOLS = [
     "moe_forward_add", "moe_dense_ffn_workspace_size", "moe_dense_ffn", "moe_dense_ffn_profiled",
     "moe_backward_workspace_size", "moe_backward", "moe_backward_launch_count", "moe_gather_rows",
     "moe_capacity_drop", "moe_expert_capacity", "moe_selftest_wait_timeout", "moe_ep_pack", "moe_ep_unpack",
+    "moe_grouped_workspace_size", "moe_grouped_gemm", "moe_grouped_dgrad",
+    "moe_grouped_wgrad_workspace_size", "moe_grouped_wgrad",
+    "moe_ckpt_blocks", "moe_ckpt_quantize", "moe_ckpt_dequantize", "moe_act_save", "moe_act_backward",
 ]
+CKPT_BLOCK = 32
 NUM_STAGE_EVENTS = 9
 NUM_DENSE_EVENTS = 3
 STAGE_NAMES = ["route", "dispatch", "gather", "expert_up", "expert_down", "shared_up", "shared_down",
@@ -127,6 +131,17 @@ _decl("moe_selftest_wait_timeout", _i, [ctypes.c_uint64, _vp, _vp, _vp])
 _decl("moe_backward_workspace_size", _sz, [_P(LayerDesc)])
 _decl("moe_backward", _i, [_P(LayerDesc), _P(Weights), _vp, _vp, _P(Grads), _vp, _sz, _vp])
 _decl("moe_backward_launch_count", _i, [_P(LayerDesc)])
+
+_decl("moe_grouped_workspace_size", _sz, [_i, _i, _i, _i, _i])
+_decl("moe_grouped_gemm", _i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp])
+_decl("moe_grouped_dgrad", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp])
+_decl("moe_grouped_wgrad_workspace_size", _sz, [_i, _i, _i, _i, _i])
+_decl("moe_grouped_wgrad", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp])
+_decl("moe_ckpt_blocks", _i, [_i])
+_decl("moe_ckpt_quantize", _i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp])
+_decl("moe_ckpt_dequantize", _i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp])
+_decl("moe_act_save", _i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp])
+_decl("moe_act_backward", _i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp])
 
 
 def _status_name(s: int) -> str:
@@ -304,3 +319,48 @@ def moe_expert_capacity(factor, T, k, M) -> int:
 def moe_selftest_wait_timeout(limit_ns, device_status, elapsed_ns=None, stream=None):
     _check("moe_selftest_wait_timeout",
            lib.moe_selftest_wait_timeout(int(limit_ns), device_status, elapsed_ns, stream))
+
+
+def moe_grouped_workspace_size(G, N, K, rows, dtype) -> int:
+    return lib.moe_grouped_workspace_size(G, N, K, rows, dtype)
+
+
+def moe_grouped_gemm(x, w, bias, offsets, G, N, K, rows, dtype, out_dtype, y, ws, ws_bytes, stream=None):
+    _check("moe_grouped_gemm", lib.moe_grouped_gemm(x, w, bias, offsets, G, N, K, rows, dtype, out_dtype, y, ws,
+                                                    ws_bytes, stream))
+
+
+def moe_grouped_dgrad(dy, w, offsets, G, N, K, rows, dtype, out_dtype, dx, ws, ws_bytes, stream=None):
+    _check("moe_grouped_dgrad", lib.moe_grouped_dgrad(dy, w, offsets, G, N, K, rows, dtype, out_dtype, dx, ws,
+                                                      ws_bytes, stream))
+
+
+def moe_grouped_wgrad_workspace_size(G, N, K, rows, dtype) -> int:
+    return lib.moe_grouped_wgrad_workspace_size(G, N, K, rows, dtype)
+
+
+def moe_grouped_wgrad(x, dy, offsets, G, N, K, rows, dtype, accumulate, dw, db, ws, ws_bytes, stream=None):
+    _check("moe_grouped_wgrad", lib.moe_grouped_wgrad(x, dy, offsets, G, N, K, rows, dtype, accumulate, dw, db, ws,
+                                                      ws_bytes, stream))
+
+
+def moe_ckpt_blocks(cols) -> int:
+    return lib.moe_ckpt_blocks(cols)
+
+
+def moe_ckpt_quantize(src, n_rows, rows, cols, dtype, q, e, stream=None):
+    _check("moe_ckpt_quantize", lib.moe_ckpt_quantize(src, n_rows, rows, cols, dtype, q, e, stream))
+
+
+def moe_ckpt_dequantize(q, e, row_index, n_rows, rows, src_rows, cols, dtype, dst, device_status=None, stream=None):
+    _check("moe_ckpt_dequantize", lib.moe_ckpt_dequantize(q, e, row_index, n_rows, rows, src_rows, cols, dtype, dst,
+                                                          device_status, stream))
+
+
+def moe_act_save(h, n_rows, rows, I, act, dtype, src_dtype, a, q, e, stream=None):
+    _check("moe_act_save", lib.moe_act_save(h, n_rows, rows, I, act, dtype, src_dtype, a, q, e, stream))
+
+
+def moe_act_backward(q, e, da, row_w, n_rows, rows, I, act, dtype, src_dtype, dh, wa=None, dw=None, stream=None):
+    _check("moe_act_backward", lib.moe_act_backward(q, e, da, row_w, n_rows, rows, I, act, dtype, src_dtype, dh, wa,
+                                                    dw, stream))

@@ -103,6 +103,39 @@ struct SwapLaunch {
 };
 cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s);
 
+// grouped_simt.cu: the three products of a grouped linear layer with weights
+// w [G, N, K] (dtype) over row segments: y [rows, N] = x W_g^T (+ bias),
+// dx [rows, K] = dy W_g (both out_dtype), dW [G, N, K] (fp32) = dy^T x.
+enum GroupedDir : int { kGroupedFwd = 0, kGroupedDgrad = 1, kGroupedWgrad = 2 };
+struct GroupedLaunch {
+  int dir;
+  int dtype, out_dtype;
+  int G, N, K, rows;
+  const int32_t* offsets;  // device [G + 1]
+  const void* x;           // [rows, K]
+  const void* dy;          // [rows, N]
+  const void* w;
+  const void* bias;        // [G, N] or null
+  int accumulate;          // wgrad: add onto out
+  void* out;
+};
+cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s);
+// db [G, N] (fp32) (+)= column sums of dy over each segment.
+cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
+                                  int accumulate, float* db, cudaStream_t s);
+
+// ckpt.cu: activation checkpoints in 8 bits (blocks of MOE_CKPT_BLOCK columns).
+cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,
+                                 uint8_t* e, cudaStream_t s);
+cudaError_t launch_ckpt_dequantize(int dtype, const int8_t* q, const uint8_t* e, const int32_t* row_index,
+                                   const int32_t* n_rows, int rows, int src_rows, int cols, void* dst, int* status,
+                                   cudaStream_t s);
+cudaError_t launch_act_save(int dtype, int src_dtype, bool swiglu, const void* h, const int32_t* n_rows, int rows,
+                            int I, void* a, int8_t* q, uint8_t* e, cudaStream_t s);
+cudaError_t launch_act_backward(int dtype, int src_dtype, bool swiglu, const int8_t* q, const uint8_t* e,
+                                const void* da, const float* row_w, const int32_t* n_rows, int rows, int I, void* dh,
+                                void* wa, float* dw, cudaStream_t s);
+
 // simt.cu: fp32 grouped GEMM with the same epilogues (fp32 dtype path).
 struct SimtLaunch {
   int epi;

@@ -9,6 +9,7 @@
 #include "gemm_sm100.cuh"
 #include <nvtx3/nvToolsExt.h>
 
+#include "api_util.cuh"
 #include "kernels.cuh"
 
 using namespace moe;
@@ -37,39 +38,13 @@ moe_status_t check_device() {
 
 namespace {
 
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
-
-struct Carve {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    const size_t o = off;
-    off += align_up(bytes);
-    return o;
-  }
-};
-
-inline size_t esize(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
 
 // A handful of rows per expert (decode): the routed GEMMs take the
 // tokens-on-M path of run_experts.
 inline bool few_rows(const moe_layer_desc_t* d) {
   return static_cast<long long>(d->T) * d->k < 4ll * d->M;
 }
-
-inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-#define MOE_TRY(expr)                          \
-  do {                                         \
-    moe_status_t st_ = (expr);                 \
-    if (st_ != MOE_OK) return st_;             \
-  } while (0)
-#define MOE_CUDA(expr) MOE_TRY(cuda_status(expr))
-
-bool aligned_ws(const void* ws) { return (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0; }
-// bf16 tensors that the tensor-core kernels move with TMA, and the fp32
-// weight gradients they store with it, start on a 16-byte boundary.
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status_t check_router_args(int T, int D, int M, int k, int dtype, int gate) {
   if (T < 0 || D < 1 || M < 1 || k < 1) return MOE_ERR_INVALID_ARG;
@@ -204,10 +179,6 @@ FwdWs forward_layout(const moe_layer_desc_t* d) {
   L.y_sh = c.take(d->I_sh > 0 ? static_cast<size_t>(d->T) * d->D * 4 : 0);
   L.pub.total = c.off;
   return L;
-}
-
-template <typename P> inline P at(void* ws, size_t off) {
-  return reinterpret_cast<P>(static_cast<char*>(ws) + off);
 }
 
 // ------------------------------------------------------------ the stages

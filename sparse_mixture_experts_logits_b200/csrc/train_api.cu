@@ -1,0 +1,168 @@
+// C ABI of the experts' step-by-step operators: the matrix products grouped
+// by expert and the 8-bit activation checkpoints (see moe_b200.h).
+#include "api_util.cuh"
+
+using namespace moe;
+
+namespace {
+
+moe_status_t check_grouped(int G, int N, int K, int rows, int dtype) {
+  if (G < 1 || N < 1 || K < 1 || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(dtype) || G > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * K >= (1ll << 40) / G) return MOE_ERR_UNSUPPORTED;
+  if (rows >= (1 << 30) || static_cast<long long>(N) >= (1 << 30) || static_cast<long long>(K) >= (1 << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t check_out(int dtype, int out_dtype) {
+  if (!is_dtype(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  return dtype == MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_F32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+struct GroupedWs { size_t status, total; };
+GroupedWs grouped_layout() {
+  Carve c;
+  GroupedWs L;
+  L.status = c.take(4);
+  L.total = c.off;
+  return L;
+}
+
+// The arguments that the two row products share.
+moe_status_t check_rows_call(const void* a, const void* w, const int32_t* offsets, int G, int N, int K, int rows,
+                             int dtype, int out_dtype, const void* out, const void* ws, size_t ws_bytes) {
+  MOE_TRY(check_grouped(G, N, K, rows, dtype));
+  MOE_TRY(check_out(dtype, out_dtype));
+  if (rows == 0) return MOE_OK;
+  if (!a || !w || !offsets || !out || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < grouped_layout().total ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+moe_status_t check_act(int rows, int I, int act, int dtype, int src_dtype) {
+  if (rows < 0 || I < 1) return MOE_ERR_INVALID_ARG;
+  if (act != MOE_ACT_GELU_TANH && act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(dtype) || !is_dtype(src_dtype)) return MOE_ERR_UNSUPPORTED;
+  return rows >= (1 << 30) || I >= (1 << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grouped_workspace_size(int G, int N, int K, int rows, int dtype) {
+  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_layout().total : 0;
+}
+
+moe_status_t moe_grouped_gemm(const void* x, const void* w, const void* bias, const int32_t* offsets, int G, int N,
+                              int K, int rows, int dtype, int out_dtype, void* y, void* ws, size_t ws_bytes,
+                              void* stream) {
+  MOE_TRY(check_rows_call(x, w, offsets, G, N, K, rows, dtype, out_dtype, y, ws, ws_bytes));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_device());
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
+  GroupedLaunch L{};
+  L.dir = kGroupedFwd;
+  L.dtype = dtype; L.out_dtype = out_dtype;
+  L.G = G; L.N = N; L.K = K; L.rows = rows;
+  L.offsets = offsets;
+  L.x = x; L.w = w; L.bias = bias; L.out = y;
+  return cuda_status(launch_grouped_simt(L, s));
+}
+
+moe_status_t moe_grouped_dgrad(const void* dy, const void* w, const int32_t* offsets, int G, int N, int K, int rows,
+                               int dtype, int out_dtype, void* dx, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_rows_call(dy, w, offsets, G, N, K, rows, dtype, out_dtype, dx, ws, ws_bytes));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_device());
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
+  GroupedLaunch L{};
+  L.dir = kGroupedDgrad;
+  L.dtype = dtype; L.out_dtype = out_dtype;
+  L.G = G; L.N = N; L.K = K; L.rows = rows;
+  L.offsets = offsets;
+  L.dy = dy; L.w = w; L.out = dx;
+  return cuda_status(launch_grouped_simt(L, s));
+}
+
+size_t moe_grouped_wgrad_workspace_size(int G, int N, int K, int rows, int dtype) {
+  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_layout().total : 0;
+}
+
+moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* offsets, int G, int N, int K, int rows,
+                               int dtype, int accumulate, float* dw, float* db, void* ws, size_t ws_bytes,
+                               void* stream) {
+  MOE_TRY(check_grouped(G, N, K, rows, dtype));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!dw) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) {
+    if (accumulate) return MOE_OK;
+    MOE_TRY(check_device());
+    MOE_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(G) * N * K * 4, s));
+    if (db) MOE_CUDA(cudaMemsetAsync(db, 0, static_cast<size_t>(G) * N * 4, s));
+    return MOE_OK;
+  }
+  if (!x || !dy || !offsets || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_grouped_wgrad_workspace_size(G, N, K, rows, dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
+  GroupedLaunch L{};
+  L.dir = kGroupedWgrad;
+  L.dtype = dtype; L.out_dtype = MOE_DTYPE_F32;
+  L.G = G; L.N = N; L.K = K; L.rows = rows;
+  L.offsets = offsets;
+  L.x = x; L.dy = dy; L.out = dw;
+  L.accumulate = accumulate != 0;
+  MOE_CUDA(launch_grouped_simt(L, s));
+  if (db) MOE_CUDA(launch_grouped_colsum(dtype, dy, offsets, G, rows, N, accumulate != 0, db, s));
+  return MOE_OK;
+}
+
+int moe_ckpt_blocks(int cols) { return cols < 1 ? 0 : (cols - 1) / MOE_CKPT_BLOCK + 1; }
+
+moe_status_t moe_ckpt_quantize(const void* src, const int32_t* n_rows, int rows, int cols, int dtype, int8_t* q,
+                               uint8_t* e, void* stream) {
+  MOE_TRY(check_act(rows, cols, MOE_ACT_GELU_TANH, dtype, dtype));
+  if (rows == 0) return MOE_OK;
+  if (!src || !q || !e) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_ckpt_quantize(dtype, src, n_rows, rows, cols, q, e, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_dequantize(const int8_t* q, const uint8_t* e, const int32_t* row_index, const int32_t* n_rows,
+                                 int rows, int src_rows, int cols, int dtype, void* dst, int32_t* device_status,
+                                 void* stream) {
+  MOE_TRY(check_act(rows, cols, MOE_ACT_GELU_TANH, dtype, dtype));
+  if (src_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!q || !e || !dst) return MOE_ERR_INVALID_ARG;
+  if (row_index == nullptr && rows > src_rows) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_ckpt_dequantize(dtype, q, e, row_index, n_rows, rows, src_rows, cols, dst, device_status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_act_save(const void* h, const int32_t* n_rows, int rows, int I, int act, int dtype, int src_dtype,
+                          void* a, int8_t* q, uint8_t* e, void* stream) {
+  MOE_TRY(check_act(rows, I, act, dtype, src_dtype));
+  if (rows == 0) return MOE_OK;
+  if (!h || !a || !q || !e) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_act_save(dtype, src_dtype, act == MOE_ACT_SWIGLU, h, n_rows, rows, I, a, q, e,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_act_backward(const int8_t* q, const uint8_t* e, const void* da, const float* row_w,
+                              const int32_t* n_rows, int rows, int I, int act, int dtype, int src_dtype, void* dh,
+                              void* wa, float* dw, void* stream) {
+  MOE_TRY(check_act(rows, I, act, dtype, src_dtype));
+  if (rows == 0) return MOE_OK;
+  if (!q || !e || !da || !dh) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_act_backward(dtype, src_dtype, act == MOE_ACT_SWIGLU, q, e, da, row_w, n_rows, rows, I,
+                                         dh, wa, dw, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
