@@ -53,12 +53,17 @@ enum GemmEpilogue : int {
   EPI_BWD_SWIGLU_DACT = 10, // G = acc, g = aux[r, n], u = aux[r, I + n], a = SiLU(g) u, da = w G:
                             //   out[., n] = da u SiLU'(g), out[., I + n] = da SiLU(g); parts += G a
   EPI_ACCUM_F32 = 11,       // out fp32 += acc   (the router's dx onto the shared expert's)
+  // Grouped products (tokens-on-N kernel only): out fp32 = acc (+ bias[g, n]),
+  // the contraction taken out of the tensor cores every kSwChunk k-blocks.
+  EPI_OUT_F32 = 12,
 };
 
 // Operand layouts of the tokens-on-N GEMM (gemm_swap_sm100.cuh): the forward
-// (both operands K-major), the input gradients (weights MN-major) and the
-// weight gradients (both MN-major, groups over the contraction).
-enum SwapLayout : int { kSwFwd = 0, kSwDgrad = 1, kSwWgrad = 2 };
+// (both operands K-major), the input gradients (weights MN-major), the
+// weight gradients (both MN-major, groups over the contraction) of padded
+// segments, and those of segments of any length.
+enum SwapLayout : int { kSwFwd = 0, kSwDgrad = 1, kSwWgrad = 2, kSwWgradRagged = 3 };
+constexpr bool is_wgrad(int layout) { return layout == kSwWgrad || layout == kSwWgradRagged; }
 
 constexpr int kBK = 64;
 constexpr int kATileBytes = 128 * kBK * 2;  // 16 KB: 128 rows of A per CTA

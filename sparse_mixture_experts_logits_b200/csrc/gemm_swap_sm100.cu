@@ -105,6 +105,8 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
   if (layout == kSwDgrad) {
     switch (epi) {
       case EPI_STORE_F32: return launch_swap_epi<EPI_STORE_F32, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_STORE_BF16: return launch_swap_epi<EPI_STORE_BF16, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_GELU_DACT: return launch_swap_epi<EPI_BWD_GELU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_SWIGLU_DACT: return launch_swap_epi<EPI_BWD_SWIGLU_DACT, kSwDgrad>(m, a, tiles_ub, s);
     }
@@ -120,6 +122,7 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     case EPI_STORE_BF16: return launch_swap_epi<EPI_STORE_BF16>(m, a, tiles_ub, s);
     case EPI_BIAS_ADD: return launch_swap_epi<EPI_BIAS_ADD>(m, a, tiles_ub, s);
     case EPI_ACCUM_F32: return launch_swap_epi<EPI_ACCUM_F32>(m, a, tiles_ub, s);
+    case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32>(m, a, tiles_ub, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -132,8 +135,14 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   // B: K-major token rows (128-row boxes), or (weight gradients) MN-major.
   const int a_inner = L.layout == kSwFwd ? L.K : L.a_cols;
   if (!tmap_bf16(&m.w, L.W, L.w_rows, a_inner, 64)) return cudaErrorInvalidValue;
-  if (L.layout == kSwWgrad) {
+  if (is_wgrad(L.layout)) {
     if (!tmap_bf16(&m.x, L.X, L.x_rows, L.b_cols, 64)) return cudaErrorInvalidValue;
+    if (L.layout == kSwWgradRagged) {
+      const long long tail_rows = static_cast<long long>(L.num_groups) * kBK;
+      if (!tmap_bf16(&m.w_tail, L.W_tail, tail_rows, L.a_cols, 64) ||
+          !tmap_bf16(&m.x_tail, L.X_tail, tail_rows, L.b_cols, 64))
+        return cudaErrorInvalidValue;
+    }
     if (L.num_groups > 1 && L.out_gstride < static_cast<long long>(L.b_cols) * L.ldo) return cudaErrorInvalidValue;
     if (!tmap_f32_out(&m.out, L.out, L.out_cols, L.b_cols, L.num_groups, L.ldo,
                       L.num_groups > 1 ? L.out_gstride : static_cast<long long>(L.b_cols) * L.ldo))
@@ -173,8 +182,13 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   a.half_cols = L.half_cols;
   a.counts = L.counts;
   a.tile_ctr = L.tile_ctr;
-  if (L.layout == kSwWgrad) {
+  a.accumulate = L.accumulate;
+  if (is_wgrad(L.layout)) {
     const long long tiles_ub = static_cast<long long>(L.num_groups) * L.w_tiles * L.b_tiles;
+    if (L.layout == kSwWgradRagged) {
+      if (L.epi != EPI_OUT_F32) return cudaErrorInvalidValue;
+      return launch_swap_epi<EPI_OUT_F32, kSwWgradRagged>(m, a, tiles_ub, s);
+    }
     if (L.epi != EPI_STORE_F32) return cudaErrorInvalidValue;
     return launch_swap_epi<EPI_STORE_F32, kSwWgrad>(m, a, tiles_ub, s);
   }

@@ -47,6 +47,20 @@
 //             .. offsets[g+1], a multiple of 64 rows whose padding rows are
 //             zero) gives out[g] = A_g^T B_g, the weight gradients of the
 //             backward.  Every output tile covers 256 A columns x 256 B columns.
+//   kSwWgradRagged  kSwWgrad over segments of any length.  A TMA box of 64 rows
+//             would run past a segment's end into the next expert's rows, so
+//             the last, partial k-block of group g is read from tail buffers
+//             instead (rows g * 64 .. of [G * 64, cols], the segment's last
+//             rows followed by zeros), which the caller fills beforehand: at
+//             most 64 (a_cols + b_cols) 2-byte elements a group, about 1% of
+//             its a_cols x b_cols fp32 outputs at model sizes.
+//
+// The tensor cores' fp32 adds truncate, which biases a long sum: measured
+// 1e-9 of the result per term (2e-6 at 2048 terms, 9e-6 at 8192).  Outputs
+// that are kept in fp32 (EPI_OUT_F32) are therefore summed in chunks of
+// kSwChunk k-blocks = 512 terms (5e-7): each chunk has a TMEM accumulator of
+// its own, and the epilogue warps add it, with rounding, to sums in their
+// registers while the next chunk's MMAs fill the other accumulator.
 #pragma once
 
 #include "gemm_sm100.cuh"
@@ -57,6 +71,7 @@ namespace moe {
 // waits once and commits once per stage.  Two k-blocks per stage (3 stages
 // of 64 KB) measured faster than one (6 stages of 32 KB) and than three.
 constexpr int kSwKB = 2;
+constexpr int kSwChunk = 8;
 constexpr int kSwStages = 3;
 constexpr int kSwATileBytes = 128 * kBK * 2;  // 128 weight rows per CTA, one k-block
 constexpr int kSwBTileBytes = 128 * kBK * 2;  // up to 128 token rows per CTA, one k-block
@@ -74,7 +89,9 @@ static_assert(kBK == 64, "the MMA loop issues four K = 16 slices per stage");
 struct SwapMaps {
   CUtensorMap w;    // A operand
   CUtensorMap x;    // B operand
-  CUtensorMap out;  // kSwWgrad: fp32 [G][b_cols][out_cols] output, 32 x 32 boxes
+  CUtensorMap out;  // weight gradients: fp32 [G][b_cols][out_cols] output, 32 x 32 boxes
+  CUtensorMap w_tail;  // kSwWgradRagged: the tail rows of both operands
+  CUtensorMap x_tail;
 };
 
 // The weight-gradient layout contracts over an expert's rows only (a few
@@ -144,6 +161,7 @@ struct SwapArgs {
   // CTA pairs claim tiles from it in index order as they become free
   // (dynamic schedule); otherwise they take fixed rounds (swap_tile_at).
   int* tile_ctr;
+  int accumulate;  // kSwWgradRagged: add onto the output
 };
 
 // Token tiles of a segment of `cnt` rows: ceil(cnt / 256) tiles of equal
@@ -174,7 +192,7 @@ struct SwapTile {
 // 256 x 256 output tiles of a group that has rows.
 template <int LAYOUT>
 __device__ __forceinline__ int swap_group_tiles(int cnt, const SwapArgs& a) {
-  if constexpr (LAYOUT == kSwWgrad) return cnt > 0 ? a.w_tiles * a.b_tiles : 0;
+  if constexpr (is_wgrad(LAYOUT)) return cnt > 0 ? a.w_tiles * a.b_tiles : 0;
   int width, ntt;
   token_tiling(cnt, width, ntt);
   return ntt * a.w_tiles;
@@ -192,7 +210,7 @@ __device__ __forceinline__ SwapTile swap_decode(int tile, int G, const int* s_ts
   SwapTile t;
   t.g = lo;
   const int cnt = s_cnt[lo];
-  if constexpr (LAYOUT == kSwWgrad) {
+  if constexpr (is_wgrad(LAYOUT)) {
     const int local = tile - s_tstart[lo];
     t.wt = local % w_tiles;
     const int bt = local / w_tiles;
@@ -267,10 +285,12 @@ __device__ __forceinline__ float warp_transpose_sum(float (&v)[32], int lane) {
 template <int EPI, int LAYOUT>
 __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
     moe_gemm_swap_kernel(const __grid_constant__ SwapMaps maps, const SwapArgs args) {
-  constexpr int S = LAYOUT == kSwWgrad ? kSwWgStages : kSwStages;
+  constexpr bool kWgrad = is_wgrad(LAYOUT);
+  constexpr bool kChunked = EPI == EPI_OUT_F32;
+  constexpr int S = kWgrad ? kSwWgStages : kSwStages;
   constexpr bool kSwiglu = EPI == EPI_SWIGLU || EPI == EPI_BWD_SWIGLU_SAVE;
   constexpr bool kAMn = LAYOUT != kSwFwd;
-  constexpr bool kBMn = LAYOUT == kSwWgrad;
+  constexpr bool kBMn = kWgrad;
   static_assert(!(kSwiglu && LAYOUT != kSwFwd), "the gate/up pairing reads K-major weight rows");
   extern __shared__ uint8_t dyn_smem[];
   __shared__ int s_off[kMaxExperts + 1];
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       fence_mbar_init();
       tma_prefetch_desc(&maps.w);
       tma_prefetch_desc(&maps.x);
-      if constexpr (LAYOUT == kSwWgrad) tma_prefetch_desc(&maps.out);
+      if constexpr (kWgrad) tma_prefetch_desc(&maps.out);
     }
   } else if (warp == 1) {
     tmem_alloc_pair(smem_addr(&s_tmem_base), 512);
@@ -479,6 +499,17 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
             const int kc = (kb0 + i) * kBK;
             const uint32_t ai = sa + i * kSwATileBytes;
             const uint32_t bi = sb + i * kSwBTileBytes;
+            if constexpr (LAYOUT == kSwWgradRagged) {
+              const bool tail = kc + kBK > s_cnt[t.g];
+              const CUtensorMap* wm = tail ? &maps.w_tail : &maps.w;
+              const CUtensorMap* xm = tail ? &maps.x_tail : &maps.x;
+              const int kr = tail ? t.g * kBK : k_row0 + kc;
+              tma_load_2d_pair(ai, wm, full_leader, w_base, kr);
+              tma_load_2d_pair(ai + 64 * kBK * 2, wm, full_leader, w_base + args.w_hi_offset, kr);
+              tma_load_2d_pair(bi, xm, full_leader, b_col, kr);
+              tma_load_2d_pair(bi + 64 * kBK * 2, xm, full_leader, b_col + 64, kr);
+              continue;
+            }
             if constexpr (!kAMn) {
               tma_load_2d_pair(ai, &maps.w, full_leader, kc, w_base);
               tma_load_2d_pair(ai + 64 * kBK * 2, &maps.w, full_leader, kc, w_base + args.w_hi_offset);
@@ -524,12 +555,31 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         if (tile >= total) break;
         const SwapTile t = swap_decode<LAYOUT>(tile, G, s_tstart, s_cnt, args, num_kb);
         const uint32_t idesc = umma_idesc_bf16_major(256, t.n, kAMn ? 1 : 0, kBMn ? 1 : 0);
-        const uint32_t buf = it & 1u;
-        const uint32_t tph = (it >> 1) & 1u;
-        if (!mbar_wait_all(smem_addr(&s_tempty[buf]), tph ^ 1u, abort_flag, args.status)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * 256u;
+        uint32_t buf = it & 1u;
+        uint32_t d_tmem = tmem_base + buf * 256u;
+        if constexpr (!kChunked) {
+          if (!mbar_wait_all(smem_addr(&s_tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, args.status)) break;
+          tc_fence_after();
+        }
         for (int kb0 = 0; kb0 < t.nkb; kb0 += kSwKB) {
+          uint32_t kb_in = static_cast<uint32_t>(kb0);  // k-block inside its accumulator
+          if constexpr (kChunked) {
+            kb_in = static_cast<uint32_t>(kb0 % kSwChunk);
+            if (kb_in == 0) {
+              if (kb0 != 0) {  // the chunk before is complete: hand it over, take the other accumulator
+                if (lane == 0) umma_commit_pair(smem_addr(&s_tfull[buf]), 0x3);
+                __syncwarp();
+                ++it;
+                buf = it & 1u;
+                d_tmem = tmem_base + buf * 256u;
+              }
+              if (!mbar_wait_all(smem_addr(&s_tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+          }
           const int nk = min(kSwKB, t.nkb - kb0);
           if (!mbar_wait_all(smem_addr(&s_full[s]), ph, abort_flag, args.status)) { ok = false; break; }
           if (lane == 0) {
@@ -539,7 +589,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
               if (i < nk) {
                 const uint64_t a = da0 + off + i * (kSwATileBytes >> 4);
                 const uint64_t b = db0 + off + i * (kSwBTileBytes >> 4);
-                umma_bf16_pair(d_tmem, a, b, idesc, (kb0 | i) != 0 ? 1u : 0u);
+                umma_bf16_pair(d_tmem, a, b, idesc, (kb_in | i) != 0 ? 1u : 0u);
                 umma_bf16_pair(d_tmem, a + kAStep, b + kBStep, idesc, 1u);
                 umma_bf16_pair(d_tmem, a + 2 * kAStep, b + 2 * kBStep, idesc, 1u);
                 umma_bf16_pair(d_tmem, a + 3 * kAStep, b + 3 * kBStep, idesc, 1u);
@@ -588,27 +638,96 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const SwapTile t = swap_decode<LAYOUT>(tile, G, s_tstart, s_cnt, args, num_kb);
       const uint32_t buf = it & 1u;
       const uint32_t tph = (it >> 1) & 1u;
-      if (!mbar_wait(smem_addr(&s_tfull[buf]), tph, abort_flag, args.status)) break;
-      tc_fence_after();
+      if constexpr (!kChunked) {
+        if (!mbar_wait(smem_addr(&s_tfull[buf]), tph, abort_flag, args.status)) break;
+        tc_fence_after();
+      }
       const int col = kSwiglu ? t.wt * args.cols_per_tile + static_cast<int>(rank) * 64 + (m & 63)
                               : t.wt * args.cols_per_tile + static_cast<int>(rank) * 128 + m;
       const bool col_ok = col < args.out_cols;
       float bias = 0.f;
       if constexpr (EPI == EPI_GELU_BIAS || EPI == EPI_SCALE_BIAS || EPI == EPI_BIAS_ADD ||
-                    EPI == EPI_BWD_GELU_SAVE) {
+                    EPI == EPI_BWD_GELU_SAVE || (EPI == EPI_OUT_F32 && !kWgrad)) {
         if (args.bias != nullptr && col_ok)
           bias = __bfloat162float(args.bias[static_cast<size_t>(t.g) * args.out_cols + col]);
       }
       // output row of the tile's first token (kSwWgrad: the first B column of
       // the tile, in group g's own output block)
-      const size_t row0 = LAYOUT == kSwWgrad ? static_cast<size_t>(t.tok0)
-                                             : static_cast<size_t>(s_off[t.g]) + t.tok0;
-      const size_t gofs = LAYOUT == kSwWgrad ? static_cast<size_t>(t.g) * args.out_gstride : 0;
+      const size_t row0 = kWgrad ? static_cast<size_t>(t.tok0) : static_cast<size_t>(s_off[t.g]) + t.tok0;
+      const size_t gofs = kWgrad ? static_cast<size_t>(t.g) * args.out_gstride : 0;
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256u;
       constexpr bool kScaled = EPI == EPI_SCALE_BIAS || EPI == EPI_BWD_GELU_SAVE ||
                                EPI == EPI_BWD_SWIGLU_SAVE || EPI == EPI_BWD_GELU_DACT ||
                                EPI == EPI_BWD_SWIGLU_DACT;
       constexpr bool kDact = EPI == EPI_BWD_GELU_DACT || EPI == EPI_BWD_SWIGLU_DACT;
+      if constexpr (kChunked) {
+        // The tile's sums in registers: this lane's column of the warp's up
+        // to four 32-row (weight gradients: 32-B-column) pieces.
+        constexpr int kPieces = kSwMaxTile / (32 * kParts);
+        float sum[kPieces][32];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSwChunk) {
+          if (kb0 != 0) ++it;
+          const uint32_t cb = it & 1u;
+          if (!mbar_wait_all(smem_addr(&s_tfull[cb]), (it >> 1) & 1u, abort_flag, args.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ca = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cb * 256u;
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            const int c = 32 * (part + kParts * j);
+            if (c < t.n) {
+              uint32_t r[32];
+              MOE_TMEM_LD32(ca + c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[j][i] += __uint_as_float(r[i]);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive_remote(cb ? tempty1 : tempty0);
+        }
+        if (!ok) break;
+        if constexpr (!kWgrad) {
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            const int c = 32 * (part + kParts * j);
+            const int nv = col_ok ? min(32, t.nrows - c) : 0;
+            float* op = static_cast<float*>(args.out) + (row0 + c) * args.ldo + col;
+            const size_t ld = args.ldo;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, op += ld)
+              if (i < nv) *op = sum[j][i] + bias;
+          }
+        } else {
+          // staged and sent out as in kSwWgrad below; accumulating tiles are
+          // added to memory by the store itself (one add per element and launch)
+          const int col0 = col - lane;
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            const int c = 32 * (part + kParts * j);
+            if (col0 < args.out_cols && c < t.nrows) {
+              const uint32_t b = sc & 1u;
+              if (lane == 0) bulk_wait_group_read<1>();
+              __syncwarp();
+              float* st = stgp + b * (kSwWgStageBufBytes / 4);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) st[i * 32 + lane] = sum[j][i];
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (args.accumulate) tma_reduce_add_3d(&maps.out, stg + b * kSwWgStageBufBytes, col0, t.tok0 + c, t.g);
+                else tma_store_3d(&maps.out, stg + b * kSwWgStageBufBytes, col0, t.tok0 + c, t.g);
+                bulk_commit_group();
+              }
+              ++sc;
+            }
+          }
+        }
+        continue;
+      }
       if constexpr (LAYOUT == kSwWgrad) {
         // Weight gradients: the warp's four 32 x 32 chunks (N = 256) are read
         // from TMEM two at a time, one wait per pair, written to a staging
@@ -792,7 +911,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       tc_fence_before();
       mbar_arrive_remote(buf ? tempty1 : tempty0);
     }
-    if constexpr (LAYOUT == kSwWgrad) {
+    if constexpr (kWgrad) {
       // the staged chunks are read and written before shared memory is released
       if (lane == 0) bulk_wait_group<0>();
       __syncwarp();

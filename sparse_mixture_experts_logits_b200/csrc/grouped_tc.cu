@@ -1,0 +1,115 @@
+// Matrix products grouped by expert on the tensor cores: bf16 operands whose
+// rows are whole 16-byte units (N and K multiples of 8).  The three products
+// are the three operand layouts of the tokens-on-N GEMM; this file gives each
+// its launch, and prepares the ragged weight gradient.
+#include <algorithm>
+
+#include "gemm_sm100.cuh"
+#include "kernels.cuh"
+
+namespace moe {
+namespace {
+
+constexpr size_t kHead = 256;  // status word and tile counters
+constexpr int kTail = kBK;     // rows of a group's tail buffer: one k-block
+
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Before a ragged weight gradient.  For group g = blockIdx.y with rows
+// [b, e): its last (e - b) % 64 rows of src, filled up with zero rows to 64,
+// go to tail[g * 64 ..]; a group without rows gets its `out` zeroed unless it
+// is added onto.  blockIdx.x shares the 16-byte units of each; blockIdx.z
+// picks the operand.
+__global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restrict__ x, const uint4* __restrict__ dy,
+                                                            const int32_t* __restrict__ offsets, int rows, int vk,
+                                                            int vn, long long out_units, int accumulate,
+                                                            uint4* __restrict__ x_tail, uint4* __restrict__ dy_tail,
+                                                            uint4* __restrict__ out) {
+  const int g = blockIdx.y;
+  const int b = max(0, min(offsets[g], rows)), e = max(0, min(offsets[g + 1], rows));
+  const int tid = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if (e <= b) {
+    if (accumulate) return;
+    uint4* o = out + g * out_units;
+    for (long long i = static_cast<long long>(blockIdx.z) * step + tid; i < out_units; i += 2ll * step) o[i] = zero;
+    return;
+  }
+  const int t = (e - b) & (kTail - 1);
+  if (t == 0) return;
+  const int v = blockIdx.z ? vn : vk;
+  const uint4* src = (blockIdx.z ? dy : x) + static_cast<long long>(e - t) * v;
+  uint4* dst = (blockIdx.z ? dy_tail : x_tail) + static_cast<long long>(g) * kTail * v;
+  for (int i = tid; i < kTail * v; i += step) dst[i] = i < t * v ? src[i] : zero;
+}
+
+}  // namespace
+
+bool grouped_tc_ok(int dtype, int N, int K) { return dtype == MOE_DTYPE_BF16 && N % 8 == 0 && K % 8 == 0; }
+
+size_t grouped_tc_workspace(int dir, int G, int N, int K) {
+  if (dir != kGroupedWgrad) return kHead;
+  const size_t rows = static_cast<size_t>(G) * kTail * 2;
+  return kHead + up256(rows * K) + up256(rows * N);
+}
+
+cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) {
+  char* base = static_cast<char*>(ws);
+  const long long wrows = static_cast<long long>(L.G) * L.N;
+  SwapLaunch S{};
+  S.num_groups = L.G;
+  S.offsets = L.offsets;
+  S.rows = L.rows;
+  S.status = reinterpret_cast<int*>(base);
+  S.w_tile_step = 256; S.w_hi_offset = 64; S.w_cta_step = 128;
+  S.cols_per_tile = 256;
+  S.out = L.out;
+  if (L.dir == kGroupedWgrad) {
+    char* x_tail = base + kHead;
+    char* dy_tail = x_tail + up256(static_cast<size_t>(L.G) * kTail * 2 * L.K);
+    const int vk = L.K / 8, vn = L.N / 8;
+    const long long units = static_cast<long long>(L.N) * L.K / 4;
+    const long long most = std::max<long long>(kTail * static_cast<long long>(std::max(vk, vn)), units / 2);
+    const int share = static_cast<int>(std::max<long long>(1, std::min<long long>((most + 1023) / 1024, 32)));
+    wgrad_prepare_kernel<<<dim3(share, L.G, 2), 256, 0, s>>>(
+        static_cast<const uint4*>(L.x), static_cast<const uint4*>(L.dy), L.offsets, L.rows, vk, vn, units,
+        L.accumulate, reinterpret_cast<uint4*>(x_tail), reinterpret_cast<uint4*>(dy_tail), static_cast<uint4*>(L.out));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // A = x (the output's contiguous index), B = dy: dw[g][n][k]
+    S.epi = EPI_OUT_F32;
+    S.layout = kSwWgradRagged;
+    S.W = L.x; S.w_rows = L.rows; S.a_cols = L.K;
+    S.X = L.dy; S.x_rows = L.rows; S.b_cols = L.N;
+    S.W_tail = x_tail; S.X_tail = dy_tail;
+    S.w_tiles = (L.K + 255) / 256;
+    S.b_tiles = (L.N + 255) / 256;
+    S.out_cols = L.K; S.ldo = L.K;
+    S.out_gstride = static_cast<long long>(L.N) * L.K;
+    S.accumulate = L.accumulate;
+    return launch_gemm_swap(S, s);
+  }
+  S.W = L.w; S.w_rows = wrows;
+  S.tile_ctr = reinterpret_cast<int*>(base) + 2;
+  if (L.dir == kGroupedDgrad) {
+    S.layout = kSwDgrad;
+    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_STORE_BF16 : EPI_OUT_F32;
+    S.X = L.dy; S.x_rows = L.rows;
+    S.K = L.N;
+    S.k_rows_per_group = L.N;
+    S.a_cols = L.K;
+    S.out_cols = L.K; S.ldo = L.K;
+  } else {
+    S.layout = kSwFwd;
+    S.epi = L.out_dtype != MOE_DTYPE_BF16 ? EPI_OUT_F32 : L.bias != nullptr ? EPI_BIAS_ADD : EPI_STORE_BF16;
+    S.X = L.x; S.x_rows = L.rows;
+    S.K = L.K;
+    S.w_rows_per_group = L.N;
+    S.out_cols = L.N; S.ldo = L.N;
+    S.bias = L.bias;
+  }
+  S.w_tiles = (S.out_cols + 255) / 256;
+  return launch_gemm_swap(S, s);
+}
+
+}  // namespace moe

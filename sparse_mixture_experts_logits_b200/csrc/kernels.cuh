@@ -100,6 +100,10 @@ struct SwapLaunch {
   const int* counts;         // optional [G]: rows computed per group (segments start at offsets)
   int* tile_ctr;             // optional: 0 at launch; with many narrow groups, tiles are claimed
                              // from it as CTA pairs free up
+  // kSwWgradRagged: the tail rows of both operands ([G * 64, a_cols] and
+  // [G * 64, b_cols]), and whether the output is added onto
+  const void* W_tail; const void* X_tail;
+  int accumulate;
 };
 cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s);
 
@@ -120,6 +124,13 @@ struct GroupedLaunch {
   void* out;
 };
 cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s);
+// grouped_tc.cu: the same products of bf16 operands on the tensor cores (N and
+// K multiples of 8, tensors on 16-byte boundaries).  `ws` holds
+// grouped_tc_workspace(dir, G, N, K) bytes, its first 16 cleared before the call: the status
+// word and two tile counters.
+bool grouped_tc_ok(int dtype, int N, int K);
+size_t grouped_tc_workspace(int dir, int G, int N, int K);
+cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s);
 // db [G, N] (fp32) (+)= column sums of dy over each segment.
 cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
                                   int accumulate, float* db, cudaStream_t s);

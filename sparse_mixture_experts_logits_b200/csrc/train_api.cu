@@ -20,13 +20,15 @@ moe_status_t check_out(int dtype, int out_dtype) {
   return dtype == MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_F32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-struct GroupedWs { size_t status, total; };
-GroupedWs grouped_layout() {
-  Carve c;
-  GroupedWs L;
-  L.status = c.take(4);
-  L.total = c.off;
-  return L;
+// Bytes of a call's workspace: the head (status word, tile counters) and what
+// the tensor-core path of the product needs.
+size_t grouped_ws(int dir, int G, int N, int K, int dtype) {
+  return grouped_tc_ok(dtype, N, K) ? grouped_tc_workspace(dir, G, N, K) : kAlign;
+}
+
+moe_status_t run_grouped(const GroupedLaunch& L, void* ws, cudaStream_t s) {
+  MOE_CUDA(cudaMemsetAsync(ws, 0, 16, s));
+  return cuda_status(grouped_tc_ok(L.dtype, L.N, L.K) ? launch_grouped_tc(L, ws, s) : launch_grouped_simt(L, s));
 }
 
 // The arguments that the two row products share.
@@ -36,7 +38,8 @@ moe_status_t check_rows_call(const void* a, const void* w, const int32_t* offset
   MOE_TRY(check_out(dtype, out_dtype));
   if (rows == 0) return MOE_OK;
   if (!a || !w || !offsets || !out || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
-  return ws_bytes < grouped_layout().total ? MOE_ERR_INVALID_ARG : MOE_OK;
+  if (grouped_tc_ok(dtype, N, K) && (!al16(a) || !al16(w))) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < grouped_ws(kGroupedFwd, G, N, K, dtype) ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 moe_status_t check_act(int rows, int I, int act, int dtype, int src_dtype) {
@@ -51,7 +54,7 @@ moe_status_t check_act(int rows, int I, int act, int dtype, int src_dtype) {
 extern "C" {
 
 size_t moe_grouped_workspace_size(int G, int N, int K, int rows, int dtype) {
-  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_layout().total : 0;
+  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_ws(kGroupedFwd, G, N, K, dtype) : 0;
 }
 
 moe_status_t moe_grouped_gemm(const void* x, const void* w, const void* bias, const int32_t* offsets, int G, int N,
@@ -60,15 +63,13 @@ moe_status_t moe_grouped_gemm(const void* x, const void* w, const void* bias, co
   MOE_TRY(check_rows_call(x, w, offsets, G, N, K, rows, dtype, out_dtype, y, ws, ws_bytes));
   if (rows == 0) return MOE_OK;
   MOE_TRY(check_device());
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
   GroupedLaunch L{};
   L.dir = kGroupedFwd;
   L.dtype = dtype; L.out_dtype = out_dtype;
   L.G = G; L.N = N; L.K = K; L.rows = rows;
   L.offsets = offsets;
   L.x = x; L.w = w; L.bias = bias; L.out = y;
-  return cuda_status(launch_grouped_simt(L, s));
+  return run_grouped(L, ws, static_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_grouped_dgrad(const void* dy, const void* w, const int32_t* offsets, int G, int N, int K, int rows,
@@ -76,19 +77,17 @@ moe_status_t moe_grouped_dgrad(const void* dy, const void* w, const int32_t* off
   MOE_TRY(check_rows_call(dy, w, offsets, G, N, K, rows, dtype, out_dtype, dx, ws, ws_bytes));
   if (rows == 0) return MOE_OK;
   MOE_TRY(check_device());
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
   GroupedLaunch L{};
   L.dir = kGroupedDgrad;
   L.dtype = dtype; L.out_dtype = out_dtype;
   L.G = G; L.N = N; L.K = K; L.rows = rows;
   L.offsets = offsets;
   L.dy = dy; L.w = w; L.out = dx;
-  return cuda_status(launch_grouped_simt(L, s));
+  return run_grouped(L, ws, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_grouped_wgrad_workspace_size(int G, int N, int K, int rows, int dtype) {
-  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_layout().total : 0;
+  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_ws(kGroupedWgrad, G, N, K, dtype) : 0;
 }
 
 moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* offsets, int G, int N, int K, int rows,
@@ -105,9 +104,9 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
     return MOE_OK;
   }
   if (!x || !dy || !offsets || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < moe_grouped_wgrad_workspace_size(G, N, K, rows, dtype)) return MOE_ERR_INVALID_ARG;
+  if (grouped_tc_ok(dtype, N, K) && (!al16(x) || !al16(dy) || !al16(dw))) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < grouped_ws(kGroupedWgrad, G, N, K, dtype)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_device());
-  MOE_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));
   GroupedLaunch L{};
   L.dir = kGroupedWgrad;
   L.dtype = dtype; L.out_dtype = MOE_DTYPE_F32;
@@ -115,7 +114,7 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
   L.offsets = offsets;
   L.x = x; L.dy = dy; L.out = dw;
   L.accumulate = accumulate != 0;
-  MOE_CUDA(launch_grouped_simt(L, s));
+  MOE_TRY(run_grouped(L, ws, s));
   if (db) MOE_CUDA(launch_grouped_colsum(dtype, dy, offsets, G, rows, N, accumulate != 0, db, s));
   return MOE_OK;
 }
