@@ -56,6 +56,7 @@ enum GemmEpilogue : int {
   // Grouped products (tokens-on-N kernel only): out fp32 = acc (+ bias[g, n]),
   // the contraction taken out of the tensor cores every kSwChunk k-blocks.
   EPI_OUT_F32 = 12,
+  EPI_OUT_BF16 = 13,        // out bf16 = acc (+ bias[g, n])
 };
 
 // Operand layouts of the tokens-on-N GEMM (gemm_swap_sm100.cuh): the forward

@@ -40,15 +40,15 @@ bool tmap_bf16(CUtensorMap* map, const void* base, long long rows, int cols, int
 }
 
 // fp32 [groups][rows][cols] with row pitch `ld` and group pitch `gstride`
-// elements, 32 x 32 x 1 boxes, no swizzle: the weight-gradient output.
+// elements, boxes of 32 columns x box_rows rows, no swizzle: the weight-gradient output.
 bool tmap_f32_out(CUtensorMap* map, void* base, int cols, long long rows, int groups, long long ld,
-                  long long gstride) {
+                  long long gstride, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(groups)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 4, static_cast<cuuint64_t>(gstride) * 4};
-  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t box[3] = {32, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
@@ -105,7 +105,7 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
   if (layout == kSwDgrad) {
     switch (epi) {
       case EPI_STORE_F32: return launch_swap_epi<EPI_STORE_F32, kSwDgrad>(m, a, tiles_ub, s);
-      case EPI_STORE_BF16: return launch_swap_epi<EPI_STORE_BF16, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_GELU_DACT: return launch_swap_epi<EPI_BWD_GELU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_SWIGLU_DACT: return launch_swap_epi<EPI_BWD_SWIGLU_DACT, kSwDgrad>(m, a, tiles_ub, s);
@@ -123,6 +123,7 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     case EPI_BIAS_ADD: return launch_swap_epi<EPI_BIAS_ADD>(m, a, tiles_ub, s);
     case EPI_ACCUM_F32: return launch_swap_epi<EPI_ACCUM_F32>(m, a, tiles_ub, s);
     case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32>(m, a, tiles_ub, s);
+    case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16>(m, a, tiles_ub, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -136,7 +137,7 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   const int a_inner = L.layout == kSwFwd ? L.K : L.a_cols;
   if (!tmap_bf16(&m.w, L.W, L.w_rows, a_inner, 64)) return cudaErrorInvalidValue;
   if (is_wgrad(L.layout)) {
-    if (!tmap_bf16(&m.x, L.X, L.x_rows, L.b_cols, 64)) return cudaErrorInvalidValue;
+    if (!tmap_bf16(&m.x[0], L.X, L.x_rows, L.b_cols, 64)) return cudaErrorInvalidValue;
     if (L.layout == kSwWgradRagged) {
       const long long tail_rows = static_cast<long long>(L.num_groups) * kBK;
       if (!tmap_bf16(&m.w_tail, L.W_tail, tail_rows, L.a_cols, 64) ||
@@ -145,10 +146,12 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
     }
     if (L.num_groups > 1 && L.out_gstride < static_cast<long long>(L.b_cols) * L.ldo) return cudaErrorInvalidValue;
     if (!tmap_f32_out(&m.out, L.out, L.out_cols, L.b_cols, L.num_groups, L.ldo,
-                      L.num_groups > 1 ? L.out_gstride : static_cast<long long>(L.b_cols) * L.ldo))
+                      L.num_groups > 1 ? L.out_gstride : static_cast<long long>(L.b_cols) * L.ldo,
+                      L.layout == kSwWgradRagged ? kSwRgBufRows : 32))
       return cudaErrorInvalidValue;
-  } else if (!tmap_bf16(&m.x, L.X, L.x_rows, L.K, 128)) {
-    return cudaErrorInvalidValue;
+  } else {
+    for (int i = 0; i < kSwBoxes; ++i)
+      if (!tmap_bf16(&m.x[i], L.X, L.x_rows, L.K, swap_box_rows(i))) return cudaErrorInvalidValue;
   }
   SwapArgs a = {};
   a.num_groups = L.num_groups;

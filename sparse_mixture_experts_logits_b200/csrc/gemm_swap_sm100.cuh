@@ -80,15 +80,34 @@ constexpr int kSwXPitch = 33;                 // floats per row of the gate/up h
 constexpr int kSwXBytes = 4 * 32 * kSwXPitch * 4;
 constexpr int kSwDynSmem = kSwStages * kSwStageBytes + kSwXBytes + 1024;
 constexpr int kSwMaxTile = 256;               // tokens per tile
+
+// kSwWgradRagged's stages: five of one k-block (32 KB), and the rest of the
+// shared memory as three 2 KB store-staging buffers per epilogue warp.  An
+// expert's contraction is short (a few k-blocks a tile), so the loads of the
+// next tile have to be in flight while the last one is stored: with two
+// stages of two k-blocks its tiles waited for their loads.
+constexpr int kSwRgStages = 5;
+constexpr int kSwPrefetchKb = 6;
+constexpr int kSwRgBufs = 3;
+constexpr int kSwRgBufRows = 16;
+constexpr int kSwRgBufBytes = kSwRgBufRows * 32 * 4;
+template <int LAYOUT>
+constexpr int swap_kb() { return LAYOUT == kSwWgradRagged ? 1 : kSwKB; }
+template <int LAYOUT>
+constexpr int swap_stage_bytes() { return swap_kb<LAYOUT>() * (kSwATileBytes + kSwBTileBytes); }
+static_assert(kSwRgStages * swap_stage_bytes<kSwWgradRagged>() + 8 * kSwRgBufs * kSwRgBufBytes + 1024 <= kSwDynSmem,
+              "the ragged weight gradient's buffers fit the launch's shared memory");
 static_assert(kBK == 64, "the MMA loop issues four K = 16 slices per stage");
 
-// Tensor maps of one launch.  The token operand always moves 128 rows per
-// CTA and k-block, whatever the tile's N: a copy per exact N / 2 rows
-// (boxes of 64, 32, 16 and 8 rows) costs more in TMA instructions than the
-// rows it saves.
+// Tensor maps of one launch.  The token operand moves one box per CTA and
+// k-block: the smallest of 16, 32, 64, 96 and 128 rows that holds the tile's
+// N / 2 (several copies that add up to N / 2 rows cost more in TMA
+// instructions than the rows they save).
+constexpr int kSwBoxes = 5;
+__host__ __device__ constexpr int swap_box_rows(int i) { return i == 0 ? 128 : i == 1 ? 96 : i == 2 ? 64 : i == 3 ? 32 : 16; }
 struct SwapMaps {
-  CUtensorMap w;    // A operand
-  CUtensorMap x;    // B operand
+  CUtensorMap w;            // A operand
+  CUtensorMap x[kSwBoxes];  // B operand, boxes of swap_box_rows(i) rows (weight gradients: x[0], 64 rows)
   CUtensorMap out;  // weight gradients: fp32 [G][b_cols][out_cols] output, 32 x 32 boxes
   CUtensorMap w_tail;  // kSwWgradRagged: the tail rows of both operands
   CUtensorMap x_tail;
@@ -287,7 +306,9 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
     moe_gemm_swap_kernel(const __grid_constant__ SwapMaps maps, const SwapArgs args) {
   constexpr bool kWgrad = is_wgrad(LAYOUT);
   constexpr bool kChunked = EPI == EPI_OUT_F32;
-  constexpr int S = kWgrad ? kSwWgStages : kSwStages;
+  constexpr int S = LAYOUT == kSwWgrad ? kSwWgStages : LAYOUT == kSwWgradRagged ? kSwRgStages : kSwStages;
+  constexpr int KB = swap_kb<LAYOUT>();
+  constexpr int kStage = swap_stage_bytes<LAYOUT>();
   constexpr bool kSwiglu = EPI == EPI_SWIGLU || EPI == EPI_BWD_SWIGLU_SAVE;
   constexpr bool kAMn = LAYOUT != kSwFwd;
   constexpr bool kBMn = kWgrad;
@@ -388,7 +409,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       }
       fence_mbar_init();
       tma_prefetch_desc(&maps.w);
-      tma_prefetch_desc(&maps.x);
+      tma_prefetch_desc(&maps.x[0]);
       if constexpr (kWgrad) tma_prefetch_desc(&maps.out);
     }
   } else if (warp == 1) {
@@ -485,14 +506,19 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const int w_base = (LAYOUT == kSwFwd ? t.g * args.w_rows_per_group : 0) + t.wt * args.w_tile_step +
                          static_cast<int>(rank) * args.w_cta_step;
       const int k_row0 = LAYOUT == kSwDgrad ? t.g * args.k_rows_per_group : s_off[t.g];
-      // both CTAs' bytes of one k-block: 128 weight rows + 128 B rows each
-      constexpr uint32_t kb_bytes = 2u * (kSwATileBytes + kSwBTileBytes);
-      for (int kb0 = 0; kb0 < t.nkb; kb0 += kSwKB) {
-        const int nk = min(kSwKB, t.nkb - kb0);
+      int box = 0;
+      if constexpr (!kBMn) {
+        while (box + 1 < kSwBoxes && swap_box_rows(box + 1) * 2 >= t.n) ++box;
+      }
+      const CUtensorMap* xmap = &maps.x[box];
+      // both CTAs' bytes of one k-block: 128 weight rows and the box's B rows each
+      const uint32_t kb_bytes = 2u * (kSwATileBytes + static_cast<uint32_t>(swap_box_rows(box)) * kBK * 2u);
+      for (int kb0 = 0; kb0 < t.nkb; kb0 += KB) {
+        const int nk = min(KB, t.nkb - kb0);
         if (!mbar_wait_all(smem_addr(&s_empty[s]), ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
         if (lane == 0) {
-          const uint32_t sa = smem_base + s * kSwStageBytes;
-          const uint32_t sb = sa + kSwKB * kSwATileBytes;
+          const uint32_t sa = smem_base + s * kStage;
+          const uint32_t sb = sa + KB * kSwATileBytes;
           const uint32_t full_leader = mapa_shared(smem_addr(&s_full[s]), 0);
           if (leader) mbar_arrive_expect_tx(smem_addr(&s_full[s]), static_cast<uint32_t>(nk) * kb_bytes);
           for (int i = 0; i < nk; ++i) {
@@ -502,7 +528,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
             if constexpr (LAYOUT == kSwWgradRagged) {
               const bool tail = kc + kBK > s_cnt[t.g];
               const CUtensorMap* wm = tail ? &maps.w_tail : &maps.w;
-              const CUtensorMap* xm = tail ? &maps.x_tail : &maps.x;
+              const CUtensorMap* xm = tail ? &maps.x_tail : &maps.x[0];
               const int kr = tail ? t.g * kBK : k_row0 + kc;
               tma_load_2d_pair(ai, wm, full_leader, w_base, kr);
               tma_load_2d_pair(ai + 64 * kBK * 2, wm, full_leader, w_base + args.w_hi_offset, kr);
@@ -519,10 +545,10 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
               tma_load_2d_pair(ai + 64 * kBK * 2, &maps.w, full_leader, w_base + args.w_hi_offset, k_row0 + kc);
             }
             if constexpr (!kBMn) {
-              tma_load_2d_pair(bi, &maps.x, full_leader, kc, x_row);
+              tma_load_2d_pair(bi, xmap, full_leader, kc, x_row);
             } else {
-              tma_load_2d_pair(bi, &maps.x, full_leader, b_col, k_row0 + kc);
-              tma_load_2d_pair(bi + 64 * kBK * 2, &maps.x, full_leader, b_col + 64, k_row0 + kc);
+              tma_load_2d_pair(bi, xmap, full_leader, b_col, k_row0 + kc);
+              tma_load_2d_pair(bi + 64 * kBK * 2, xmap, full_leader, b_col + 64, k_row0 + kc);
             }
           }
         }
@@ -542,8 +568,8 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       constexpr uint64_t kAStep = kAMn ? 128 : 2;
       constexpr uint64_t kBStep = kBMn ? 128 : 2;
       const uint64_t da0 = kAMn ? sw128_mnmajor_desc(smem_base, 64 * kBK * 2) : sw128_kmajor_desc(smem_base);
-      const uint64_t db0 = kBMn ? sw128_mnmajor_desc(smem_base + kSwKB * kSwATileBytes, 64 * kBK * 2)
-                                : sw128_kmajor_desc(smem_base + kSwKB * kSwATileBytes);
+      const uint64_t db0 = kBMn ? sw128_mnmajor_desc(smem_base + KB * kSwATileBytes, 64 * kBK * 2)
+                                : sw128_kmajor_desc(smem_base + KB * kSwATileBytes);
       for (int rd = 0; ok; ++rd, ++it) {
         int tile;
         if (dyn) {
@@ -561,7 +587,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           if (!mbar_wait_all(smem_addr(&s_tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, args.status)) break;
           tc_fence_after();
         }
-        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSwKB) {
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += KB) {
           uint32_t kb_in = static_cast<uint32_t>(kb0);  // k-block inside its accumulator
           if constexpr (kChunked) {
             kb_in = static_cast<uint32_t>(kb0 % kSwChunk);
@@ -580,12 +606,12 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
               tc_fence_after();
             }
           }
-          const int nk = min(kSwKB, t.nkb - kb0);
+          const int nk = min(KB, t.nkb - kb0);
           if (!mbar_wait_all(smem_addr(&s_full[s]), ph, abort_flag, args.status)) { ok = false; break; }
           if (lane == 0) {
-            const uint64_t off = static_cast<uint64_t>(s * (kSwStageBytes >> 4));
+            const uint64_t off = static_cast<uint64_t>(s * (kStage >> 4));
 #pragma unroll
-            for (int i = 0; i < kSwKB; ++i) {
+            for (int i = 0; i < KB; ++i) {
               if (i < nk) {
                 const uint64_t a = da0 + off + i * (kSwATileBytes >> 4);
                 const uint64_t b = db0 + off + i * (kSwBTileBytes >> 4);
@@ -647,7 +673,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const bool col_ok = col < args.out_cols;
       float bias = 0.f;
       if constexpr (EPI == EPI_GELU_BIAS || EPI == EPI_SCALE_BIAS || EPI == EPI_BIAS_ADD ||
-                    EPI == EPI_BWD_GELU_SAVE || (EPI == EPI_OUT_F32 && !kWgrad)) {
+                    EPI == EPI_BWD_GELU_SAVE || EPI == EPI_OUT_BF16 || (EPI == EPI_OUT_F32 && !kWgrad)) {
         if (args.bias != nullptr && col_ok)
           bias = __bfloat162float(args.bias[static_cast<size_t>(t.g) * args.out_cols + col]);
       }
@@ -662,8 +688,22 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       constexpr bool kDact = EPI == EPI_BWD_GELU_DACT || EPI == EPI_BWD_SWIGLU_DACT;
       if constexpr (kChunked) {
         // The tile's sums in registers: this lane's column of the warp's up
-        // to four 32-row (weight gradients: 32-B-column) pieces.
+        // to four pieces of 32 rows (weight gradients: 32 B columns).
         constexpr int kPieces = kSwMaxTile / (32 * kParts);
+        if constexpr (kWgrad) {
+          // What a tile of few rows is added onto comes into L2 during its
+          // MMAs, instead of when the reducing stores ask for it at the end
+          // (48 experts x 2048 x 5120, 256 rows each: 0.89 -> 0.73 ms; the
+          // bytes alone are 0.62).  With more rows to a tile the operand
+          // loads behind the prefetches cost more than they gain (512 rows:
+          // 0.94 -> 0.96 ms).
+          if (args.accumulate && t.nkb <= kSwPrefetchKb && col - lane < args.out_cols) {
+            const float* line = static_cast<const float*>(args.out) + gofs + row0 * args.ldo + (col - lane);
+#pragma unroll 1
+            for (int c = 32 * part + lane; c < t.nrows; c += 32 * kParts)
+              prefetch_l2(line + static_cast<size_t>(c) * args.ldo);
+          }
+        }
         float sum[kPieces][32];
 #pragma unroll
         for (int j = 0; j < kPieces; ++j)
@@ -679,11 +719,15 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           for (int j = 0; j < kPieces; ++j) {
             const int c = 32 * (part + kParts * j);
             if (c < t.n) {
-              uint32_t r[32];
-              MOE_TMEM_LD32(ca + c, r);
-              tmem_ld_wait();
+              // 16 columns at a time: 32 would not leave enough registers beside the sums
 #pragma unroll
-              for (int i = 0; i < 32; ++i) sum[j][i] += __uint_as_float(r[i]);
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t r[16];
+                MOE_TMEM_LD16(ca + c + h, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[j][h + i] += __uint_as_float(r[i]);
+              }
             }
           }
           tc_fence_before();
@@ -691,38 +735,45 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         }
         if (!ok) break;
         if constexpr (!kWgrad) {
+          const size_t ld = args.ldo;
 #pragma unroll
           for (int j = 0; j < kPieces; ++j) {
             const int c = 32 * (part + kParts * j);
             const int nv = col_ok ? min(32, t.nrows - c) : 0;
-            float* op = static_cast<float*>(args.out) + (row0 + c) * args.ldo + col;
-            const size_t ld = args.ldo;
+            float* op = static_cast<float*>(args.out) + (row0 + c) * ld + col;
 #pragma unroll
             for (int i = 0; i < 32; ++i, op += ld)
               if (i < nv) *op = sum[j][i] + bias;
           }
         } else {
-          // staged and sent out as in kSwWgrad below; accumulating tiles are
-          // added to memory by the store itself (one add per element and launch)
+          // staged in the output's own layout (lane = column) and sent out by
+          // TMA, 16 output rows a box; the tensor map clips rows past b_cols
+          // and columns past out_cols.  A tile that is added onto is added by
+          // the store itself (one add per element and launch).
           const int col0 = col - lane;
+          const uint32_t rbuf = smem_base + S * kStage + (warp - 2) * kSwRgBufs * kSwRgBufBytes;
+          float* rbufp = reinterpret_cast<float*>(dyn_smem + (rbuf - smem_addr(dyn_smem)));
 #pragma unroll
           for (int j = 0; j < kPieces; ++j) {
-            const int c = 32 * (part + kParts * j);
-            if (col0 < args.out_cols && c < t.nrows) {
-              const uint32_t b = sc & 1u;
-              if (lane == 0) bulk_wait_group_read<1>();
-              __syncwarp();
-              float* st = stgp + b * (kSwWgStageBufBytes / 4);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) st[i * 32 + lane] = sum[j][i];
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (args.accumulate) tma_reduce_add_3d(&maps.out, stg + b * kSwWgStageBufBytes, col0, t.tok0 + c, t.g);
-                else tma_store_3d(&maps.out, stg + b * kSwWgStageBufBytes, col0, t.tok0 + c, t.g);
-                bulk_commit_group();
+            for (int h = 0; h < 32; h += kSwRgBufRows) {
+              const int c = 32 * (part + kParts * j) + h;
+              if (col0 < args.out_cols && c < t.nrows) {
+                if (lane == 0) bulk_wait_group_read<kSwRgBufs - 1>();  // buffer sc's last store has read it
+                __syncwarp();
+                float* st = rbufp + sc * (kSwRgBufBytes / 4);
+#pragma unroll
+                for (int i = 0; i < kSwRgBufRows; ++i) st[i * 32 + lane] = sum[j][h + i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  const uint32_t src = rbuf + sc * kSwRgBufBytes;
+                  if (args.accumulate) tma_reduce_add_3d(&maps.out, src, col0, t.tok0 + c, t.g);
+                  else tma_store_3d(&maps.out, src, col0, t.tok0 + c, t.g);
+                  bulk_commit_group();
+                }
+                sc = sc + 1 == kSwRgBufs ? 0 : sc + 1;
               }
-              ++sc;
             }
           }
         }
@@ -766,6 +817,33 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         }
       } else
       for (int c = 32 * part; c < t.n; c += 32 * kParts) {
+        if constexpr (EPI == EPI_OUT_BF16) {
+          // Four rows at a time: neighbouring lanes swap one shuffle's worth
+          // of halves, so that the even lane holds both lanes' columns of rows
+          // 0 and 2 and the odd lane those of rows 1 and 3, and each 4-byte
+          // store covers two rows' 64-byte pieces (half the store
+          // instructions of a column per lane; out_cols is even).
+          uint32_t r[32];
+          MOE_TMEM_LD32(tacc + c, r);
+          tmem_ld_wait();
+          const bool odd = (lane & 1) != 0;
+          const int nv = col_ok ? t.nrows - c : 0;
+          const size_t ld = args.ldo;
+          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(args.out) + (row0 + c + (odd ? 1 : 0)) * ld + (col & ~1);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4, op += 4 * ld) {
+            const __nv_bfloat162 e = __floats2bfloat162_rn(__uint_as_float(r[i]) + bias, __uint_as_float(r[i + 2]) + bias);
+            const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(r[i + 1]) + bias, __uint_as_float(r[i + 3]) + bias);
+            const uint32_t mine = odd ? *reinterpret_cast<const uint32_t*>(&o) : *reinterpret_cast<const uint32_t*>(&e);
+            const uint32_t give = odd ? *reinterpret_cast<const uint32_t*>(&e) : *reinterpret_cast<const uint32_t*>(&o);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;
+            const int rr = i + (odd ? 1 : 0);
+            if (rr < nv) *reinterpret_cast<uint32_t*>(op) = __byte_perm(lo, hi, 0x5410);
+            if (rr + 2 < nv) *reinterpret_cast<uint32_t*>(op + 2 * ld) = __byte_perm(lo, hi, 0x7632);
+          }
+          continue;
+        }
         // Every value this chunk reads from memory (the input-gradient
         // epilogues' saved pre-activations, the addend, the fp32 sum added
         // onto) is requested first, all 32 rows together, so that the loads

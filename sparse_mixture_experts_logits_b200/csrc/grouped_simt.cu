@@ -133,34 +133,81 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
   }
 }
 
-// db[g, n] (+)= sum over g's rows of dy[r, n].  Block (64 columns, group):
-// eight warps take every eighth row, two columns a thread, and their sums are
-// added in warp order.
+// db[g, n] (+)= sum over g's rows of dy[r, n].  A block takes `share` of the
+// segment's rows (blockIdx.z) for 64 columns: its eight warps take every
+// eighth row, two columns a thread and eight rows in flight, and their sums
+// are added in warp order.  With more than one share the blocks leave partial
+// sums [share][G][N], which grouped_colsum_join_kernel adds in order.  Bound
+// by reading dy once.
 template <typename T>
+__device__ __forceinline__ float2 ld2(const T* p, bool second);
+template <>
+__device__ __forceinline__ float2 ld2(const float* p, bool second) {
+  return make_float2(p[0], second ? p[1] : 0.f);
+}
+template <>
+__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p, bool second) {
+  return make_float2(__bfloat162float(p[0]), second ? __bfloat162float(p[1]) : 0.f);
+}
+
+template <typename T, bool PAIRED>
 __global__ void __launch_bounds__(256) grouped_colsum_kernel(const T* __restrict__ dy,
                                                              const int32_t* __restrict__ offsets, int rows, int N,
-                                                             int accumulate, float* __restrict__ db) {
-  __shared__ float s[8][64];
+                                                             int accumulate, float* __restrict__ out) {
+  __shared__ float2 s[8][32];
   const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r0 = max(0, min(offsets[g], rows)), r1 = max(0, min(offsets[g + 1], rows));
-  const int n0 = blockIdx.x * 64 + lane, n1 = n0 + 32;
-  float a = 0.f, b = 0.f;
-  for (long long r = r0 + warp; r < r1; r += 8) {
-    if (n0 < N) a += to_f32(dy[r * N + n0]);
-    if (n1 < N) b += to_f32(dy[r * N + n1]);
+  const int b = max(0, min(offsets[g], rows)), e = max(b, max(0, min(offsets[g + 1], rows)));
+  const int per = (e - b + gridDim.z - 1) / gridDim.z;
+  const int r0 = min(e, b + static_cast<int>(blockIdx.z) * per), r1 = min(e, r0 + per);
+  const int n = blockIdx.x * 64 + 2 * lane;
+  float2 a = make_float2(0.f, 0.f);
+  if (n < N) {
+    const bool two = n + 1 < N;
+    const T* p = dy + static_cast<long long>(r0 + warp) * N + n;
+    const long long step = 8ll * N;
+    int r = r0 + warp;
+    for (; r + 56 < r1; r += 64, p += 8 * step) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (PAIRED) {  // N is even and dy on a whole pair: one load for both columns
+          if constexpr (sizeof(T) == 2)
+            v[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + i * step));
+          else
+            v[i] = *reinterpret_cast<const float2*>(p + i * step);
+        } else {
+          v[i] = ld2(p + i * step, two);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) { a.x += v[i].x; a.y += v[i].y; }
+    }
+    for (; r < r1; r += 8, p += step) {
+      const float2 v = ld2(p, two);
+      a.x += v.x;
+      a.y += v.y;
+    }
   }
   s[warp][lane] = a;
-  s[warp][lane + 32] = b;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int n = blockIdx.x * 64 + threadIdx.x;
-    float v = 0.f;
+  if (warp == 0 && n < N) {
+    float2 v = s[0][lane];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][threadIdx.x];
-    if (n < N) {
-      float* o = db + static_cast<long long>(g) * N + n;
-      *o = accumulate ? *o + v : v;
-    }
+    for (int i = 1; i < 8; ++i) { v.x += s[i][lane].x; v.y += s[i][lane].y; }
+    float* o = out + (static_cast<long long>(blockIdx.z) * gridDim.y + g) * N + n;
+    o[0] = accumulate ? o[0] + v.x : v.x;
+    if (n + 1 < N) o[1] = accumulate ? o[1] + v.y : v.y;
+  }
+}
+
+__global__ void __launch_bounds__(256) grouped_colsum_join_kernel(const float* __restrict__ part, int shares,
+                                                                  long long n, int accumulate,
+                                                                  float* __restrict__ db) {
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    float v = accumulate ? db[i] : 0.f;
+    for (int z = 0; z < shares; ++z) v += part[z * n + i];
+    db[i] = v;
   }
 }
 
@@ -208,14 +255,34 @@ cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s) {
   return run<float, float, false>(a, tiles, s);
 }
 
+int grouped_colsum_shares(int G, int rows, int N) {
+  const long long blocks = static_cast<long long>((N + 63) / 64) * G;
+  // eight blocks an SM, of 128 rows of an even segment at least
+  const long long want = (8ll * 148 + blocks - 1) / blocks, most = (static_cast<long long>(rows) / G + 127) / 128;
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({want, most, 64})));
+}
+
 cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
-                                  int accumulate, float* db, cudaStream_t s) {
-  const dim3 grid((N + 63) / 64, G);
-  if (dtype == MOE_DTYPE_BF16)
-    grouped_colsum_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(dy), offsets, rows, N, accumulate,
-                                               db);
-  else
-    grouped_colsum_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(dy), offsets, rows, N, accumulate, db);
+                                  int accumulate, float* db, float* part, cudaStream_t s) {
+  const int shares = grouped_colsum_shares(G, rows, N);
+  const dim3 grid((N + 63) / 64, G, shares);
+  float* out = shares > 1 ? part : db;
+  const int acc = shares > 1 ? 0 : accumulate;
+  const bool pair = N % 2 == 0 && reinterpret_cast<uintptr_t>(dy) % 8 == 0;
+  if (dtype == MOE_DTYPE_BF16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(dy);
+    if (pair) grouped_colsum_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+    else grouped_colsum_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+  } else {
+    const float* p = static_cast<const float*>(dy);
+    if (pair) grouped_colsum_kernel<float, true><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+    else grouped_colsum_kernel<float, false><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+  }
+  if (shares > 1) {
+    const long long n = static_cast<long long>(G) * N;
+    const int blocks = static_cast<int>(std::min<long long>((n + 255) / 256, 4ll * num_sms()));
+    grouped_colsum_join_kernel<<<blocks, 256, 0, s>>>(part, shares, n, accumulate, db);
+  }
   return cudaGetLastError();
 }
 

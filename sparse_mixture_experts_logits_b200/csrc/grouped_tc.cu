@@ -93,7 +93,7 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
   S.tile_ctr = reinterpret_cast<int*>(base) + 2;
   if (L.dir == kGroupedDgrad) {
     S.layout = kSwDgrad;
-    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_STORE_BF16 : EPI_OUT_F32;
+    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;
     S.X = L.dy; S.x_rows = L.rows;
     S.K = L.N;
     S.k_rows_per_group = L.N;
@@ -101,7 +101,7 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     S.out_cols = L.K; S.ldo = L.K;
   } else {
     S.layout = kSwFwd;
-    S.epi = L.out_dtype != MOE_DTYPE_BF16 ? EPI_OUT_F32 : L.bias != nullptr ? EPI_BIAS_ADD : EPI_STORE_BF16;
+    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;
     S.X = L.x; S.x_rows = L.rows;
     S.K = L.K;
     S.w_rows_per_group = L.N;

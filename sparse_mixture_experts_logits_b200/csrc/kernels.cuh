@@ -131,9 +131,11 @@ cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s);
 bool grouped_tc_ok(int dtype, int N, int K);
 size_t grouped_tc_workspace(int dir, int G, int N, int K);
 cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s);
-// db [G, N] (fp32) (+)= column sums of dy over each segment.
+// db [G, N] (fp32) (+)= column sums of dy over each segment.  `part` holds
+// grouped_colsum_shares(...) * G * N floats when that is more than one share.
+int grouped_colsum_shares(int G, int rows, int N);
 cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
-                                  int accumulate, float* db, cudaStream_t s);
+                                  int accumulate, float* db, float* part, cudaStream_t s);
 
 // ckpt.cu: activation checkpoints in 8 bits (blocks of MOE_CKPT_BLOCK columns).
 cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,

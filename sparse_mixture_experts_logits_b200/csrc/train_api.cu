@@ -26,6 +26,18 @@ size_t grouped_ws(int dir, int G, int N, int K, int dtype) {
   return grouped_tc_ok(dtype, N, K) ? grouped_tc_workspace(dir, G, N, K) : kAlign;
 }
 
+// moe_grouped_wgrad: that, and the bias gradient's partial sums behind it.
+struct WgradWs { size_t part, total; };
+WgradWs wgrad_layout(int G, int N, int K, int rows, int dtype) {
+  Carve c;
+  WgradWs L;
+  c.take(grouped_ws(kGroupedWgrad, G, N, K, dtype));
+  const int shares = grouped_colsum_shares(G, rows, N);
+  L.part = c.take(shares > 1 ? static_cast<size_t>(shares) * G * N * 4 : 0);
+  L.total = c.off;
+  return L;
+}
+
 moe_status_t run_grouped(const GroupedLaunch& L, void* ws, cudaStream_t s) {
   MOE_CUDA(cudaMemsetAsync(ws, 0, 16, s));
   return cuda_status(grouped_tc_ok(L.dtype, L.N, L.K) ? launch_grouped_tc(L, ws, s) : launch_grouped_simt(L, s));
@@ -87,7 +99,7 @@ moe_status_t moe_grouped_dgrad(const void* dy, const void* w, const int32_t* off
 }
 
 size_t moe_grouped_wgrad_workspace_size(int G, int N, int K, int rows, int dtype) {
-  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? grouped_ws(kGroupedWgrad, G, N, K, dtype) : 0;
+  return check_grouped(G, N, K, rows, dtype) == MOE_OK ? wgrad_layout(G, N, K, rows, dtype).total : 0;
 }
 
 moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* offsets, int G, int N, int K, int rows,
@@ -105,7 +117,8 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
   }
   if (!x || !dy || !offsets || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
   if (grouped_tc_ok(dtype, N, K) && (!al16(x) || !al16(dy) || !al16(dw))) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < grouped_ws(kGroupedWgrad, G, N, K, dtype)) return MOE_ERR_INVALID_ARG;
+  const WgradWs W = wgrad_layout(G, N, K, rows, dtype);
+  if (ws_bytes < W.total) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_device());
   GroupedLaunch L{};
   L.dir = kGroupedWgrad;
@@ -115,7 +128,7 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
   L.x = x; L.dy = dy; L.out = dw;
   L.accumulate = accumulate != 0;
   MOE_TRY(run_grouped(L, ws, s));
-  if (db) MOE_CUDA(launch_grouped_colsum(dtype, dy, offsets, G, rows, N, accumulate != 0, db, s));
+  if (db) MOE_CUDA(launch_grouped_colsum(dtype, dy, offsets, G, rows, N, accumulate != 0, db, at<float*>(ws, W.part), s));
   return MOE_OK;
 }
 
