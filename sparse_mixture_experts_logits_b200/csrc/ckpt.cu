@@ -192,6 +192,265 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const int8_t* __restr
   }
 }
 
+// ------------------------- widths that are a multiple of 8: 16-byte accesses
+// A thread takes 8 consecutive columns, four neighbouring threads a block of
+// 32; `tx` = 2^lx threads (4 to 256) run along a row and the 256 / tx rows of a
+// thread block step through the batch together.  kU column steps are loaded
+// before any is used, which keeps 32 to 128 bytes a thread in flight.
+template <typename T> struct Vec8;  // 8 values as they lie in memory
+template <> struct Vec8<__nv_bfloat16> { uint4 a; };
+template <> struct Vec8<float> { float4 a, b; };
+__device__ __forceinline__ Vec8<__nv_bfloat16> load8(const __nv_bfloat16* p) {
+  return {*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ Vec8<float> load8(const float* p) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+  return {q[0], q[1]};
+}
+__device__ __forceinline__ void unpack8(const Vec8<__nv_bfloat16>& v, float* f) { bf16x8_to_f32(v.a, f); }
+__device__ __forceinline__ void unpack8(const Vec8<float>& v, float* f) {
+  f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
+  f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
+  *reinterpret_cast<uint4*>(p) = f32_to_bf16x8(f);
+}
+__device__ __forceinline__ void store8(float* p, const float* f) {
+  float4* q = reinterpret_cast<float4*>(p);
+  q[0] = make_float4(f[0], f[1], f[2], f[3]);
+  q[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// q of 8 values and the exponent byte of their block (the four threads of a
+// block exchange their largest magnitudes; every lane of the warp takes part).
+__device__ __forceinline__ uint2 keep8(const float* f, uint32_t& e) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  e = m >> 23;
+  const float inv = ckpt_inv_scale(e);
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(ckpt_q(f[i], inv)) & 0xffu;
+  return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+}
+__device__ __forceinline__ void read8(const uint2& q, uint32_t e, float* f) {
+  const float s = ckpt_scale(e);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = static_cast<float>(static_cast<int8_t>(q.x >> (8 * i))) * s;
+    f[4 + i] = static_cast<float>(static_cast<int8_t>(q.y >> (8 * i))) * s;
+  }
+}
+
+constexpr int kU = 2;
+
+template <typename T>
+__global__ void __launch_bounds__(256) ckpt_quantize_vec_kernel(const T* __restrict__ src, const int32_t* n_rows,
+                                                                int rows, int cols, int nb, int lx,
+                                                                int8_t* __restrict__ q, uint8_t* __restrict__ e) {
+  const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
+  const int n = live_rows(n_rows, rows);
+  const Vec8<T> none = {};
+  for (long long r0 = static_cast<long long>(blockIdx.x) * ny; r0 < n; r0 += static_cast<long long>(gridDim.x) * ny) {
+    const long long r = r0 + (threadIdx.x >> lx);
+    for (int c0 = 8 * x; c0 - 8 * x < cols; c0 += kU * 8 * tx) {
+      Vec8<T> v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+        v[u] = r < n && c < cols ? load8(src + r * cols + c) : none;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+        float f[8];
+        unpack8(v[u], f);
+        uint32_t ex;
+        const uint2 k = keep8(f, ex);
+        if (r < n && c < cols) {
+          *reinterpret_cast<uint2*>(q + r * cols + c) = k;
+          if ((x & 3) == 0) e[r * nb + c / kBlk] = static_cast<uint8_t>(ex);
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) ckpt_dequantize_vec_kernel(const int8_t* __restrict__ q,
+                                                                  const uint8_t* __restrict__ e,
+                                                                  const int32_t* __restrict__ row_index,
+                                                                  const int32_t* n_rows, int rows, int src_rows,
+                                                                  int cols, int nb, int lx, T* __restrict__ dst,
+                                                                  int* status) {
+  constexpr int kD = 4;
+  const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
+  const int n = live_rows(n_rows, rows);
+  for (long long r = static_cast<long long>(blockIdx.x) * ny + (threadIdx.x >> lx); r < n;
+       r += static_cast<long long>(gridDim.x) * ny) {
+    const long long sr = row_index != nullptr ? row_index[r] : r;
+    const bool ok = sr >= 0 && sr < src_rows;
+    if (!ok && x == 0) set_status(status, MOE_DEVERR_BAD_ROW_TOKEN);
+    for (int c0 = 8 * x; c0 < cols; c0 += kD * 8 * tx) {
+      uint2 k[kD];
+      uint32_t ex[kD];
+#pragma unroll
+      for (int u = 0; u < kD; ++u) {
+        const int c = c0 + u * 8 * tx;
+        const bool on = ok && c < cols;
+        k[u] = on ? *reinterpret_cast<const uint2*>(q + sr * cols + c) : make_uint2(0u, 0u);
+        ex[u] = on ? e[sr * nb + c / kBlk] : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < kD; ++u) {
+        const int c = c0 + u * 8 * tx;
+        float f[8];
+        read8(k[u], ex[u], f);
+        if (c < cols) store8(dst + r * cols + c, f);
+      }
+    }
+  }
+}
+
+template <typename TS, typename TD, bool SWIGLU>
+__global__ void __launch_bounds__(256) act_save_vec_kernel(const TS* __restrict__ h, const int32_t* n_rows, int rows,
+                                                           int I, int nb, int lx, TD* __restrict__ a,
+                                                           int8_t* __restrict__ q, uint8_t* __restrict__ e) {
+  constexpr int H = SWIGLU ? 2 : 1;
+  const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
+  const int n = live_rows(n_rows, rows);
+  const Vec8<TS> none = {};
+  for (long long r0 = static_cast<long long>(blockIdx.x) * ny; r0 < n; r0 += static_cast<long long>(gridDim.x) * ny) {
+    const long long r = r0 + (threadIdx.x >> lx);
+    for (int c0 = 8 * x; c0 - 8 * x < I; c0 += kU * 8 * tx) {
+      Vec8<TS> v[kU][H];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[u][j] = r < n && c < I ? load8(h + (r * H + j) * I + c) : none;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+        const bool on = r < n && c < I;
+        float f[H][8], o[8];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          unpack8(v[u][j], f[j]);
+          uint32_t ex;
+          const uint2 k = keep8(f[j], ex);
+          if (on) {
+            *reinterpret_cast<uint2*>(q + (r * H + j) * I + c) = k;
+            if ((x & 3) == 0) e[(r * H + j) * nb + c / kBlk] = static_cast<uint8_t>(ex);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (SWIGLU) o[i] = swiglu(f[0][i], f[1][i]);
+          else o[i] = gelu_sig(f[0][i]);
+        }
+        if (on) store8(a + r * I + c, o);
+      }
+    }
+  }
+}
+
+template <typename TS, typename TD, bool SWIGLU>
+__global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __restrict__ q,
+                                                               const uint8_t* __restrict__ e,
+                                                               const TS* __restrict__ da,
+                                                               const float* __restrict__ row_w, const int32_t* n_rows,
+                                                               int rows, int I, int nb, int lx, TD* __restrict__ dh,
+                                                               TD* __restrict__ wa, float* __restrict__ dw) {
+  constexpr int H = SWIGLU ? 2 : 1;
+  __shared__ float s_part[8];
+  const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
+  const int n = live_rows(n_rows, rows);
+  const Vec8<TS> none = {};
+  for (long long r0 = static_cast<long long>(blockIdx.x) * ny; r0 < n; r0 += static_cast<long long>(gridDim.x) * ny) {
+    const long long r = r0 + (threadIdx.x >> lx);
+    const bool live = r < n;
+    const float w = live && row_w != nullptr ? row_w[r] : 1.0f;
+    float dot = 0.0f;
+    for (int c0 = 8 * x; c0 < I; c0 += kU * 8 * tx) {
+      uint2 k[kU][H];
+      uint32_t ex[kU][H];
+      Vec8<TS> v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+        const bool on = live && c < I;
+        v[u] = on ? load8(da + r * I + c) : none;
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          k[u][j] = on ? *reinterpret_cast<const uint2*>(q + (r * H + j) * I + c) : make_uint2(0u, 0u);
+          ex[u][j] = on ? e[(r * H + j) * nb + c / kBlk] : 0u;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * 8 * tx;
+        const bool on = live && c < I;
+        float g[8], f[H][8], d[H][8], o[8];
+        unpack8(v[u], g);
+#pragma unroll
+        for (int j = 0; j < H; ++j) read8(k[u][j], ex[u][j], f[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float act;
+          if constexpr (SWIGLU) swiglu_grad(f[0][i], f[1][i], act, d[0][i], d[1][i]);
+          else gelu_sig_grad(f[0][i], act, d[0][i]);
+          dot = fmaf(g[i], act, dot);
+          o[i] = w * act;
+#pragma unroll
+          for (int j = 0; j < H; ++j) d[j][i] *= w * g[i];
+        }
+        if (on) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) store8(dh + (r * H + j) * I + c, d[j]);
+          if (wa != nullptr) store8(wa + r * I + c, o);
+        }
+      }
+    }
+    if (dw != nullptr) {
+      // a row's threads are one aligned part of a warp, or whole warps: the
+      // sum runs over the part, then over the warps in order
+      for (int o = min(tx, 32) >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (tx > 32) {
+        if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        if (x == 0) {
+          dot = 0.0f;
+          for (int i = 0; i < (tx >> 5); ++i) dot += s_part[(threadIdx.x >> 5) + i];
+        }
+        __syncthreads();
+      }
+      if (x == 0 && live) dw[r] = dot;
+    }
+  }
+}
+
+// Threads along a row (as a power of two) and the grid.  A row's threads are
+// at most one warp when there are rows enough to fill the GPU (no block-wide
+// reduction for dw, long runs per thread); few rows spread over up to 256.
+struct Shape { int lx, grid; };
+inline Shape shape(int rows, int cols) {
+  int lx = 2;
+  const int most = rows >= 16 * num_sms() ? 5 : 8;
+  while (lx < most && (8 << lx) < cols) ++lx;
+  const int ny = 256 >> lx;
+  return {lx, std::min((rows - 1) / ny + 1, 8 * num_sms())};
+}
+inline bool vec_ok(int cols, const void* a, const void* b, const void* c, const void* d) {
+  const uintptr_t any = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                        reinterpret_cast<uintptr_t>(c) | reinterpret_cast<uintptr_t>(d);
+  return cols % 8 == 0 && any % 16 == 0;
+}
+
 inline int warp_grid(long long units) {
   return static_cast<int>(std::max<long long>(1, std::min<long long>((units + 7) / 8, 8ll * num_sms())));
 }
@@ -202,6 +461,16 @@ inline int blocks_of(int cols) { return (cols + kBlk - 1) / kBlk; }
 cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,
                                  uint8_t* e, cudaStream_t s) {
   const int nb = blocks_of(cols), grid = warp_grid(static_cast<long long>(rows) * nb);
+  if (vec_ok(cols, src, q, nullptr, nullptr)) {
+    const Shape p = shape(rows, cols);
+    if (dtype == MOE_DTYPE_BF16)
+      ckpt_quantize_vec_kernel<<<p.grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src), n_rows, rows, cols, nb,
+                                                      p.lx, q, e);
+    else
+      ckpt_quantize_vec_kernel<<<p.grid, 256, 0, s>>>(static_cast<const float*>(src), n_rows, rows, cols, nb, p.lx, q,
+                                                      e);
+    return cudaGetLastError();
+  }
   if (dtype == MOE_DTYPE_BF16)
     ckpt_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src), n_rows, rows, cols, nb, q, e);
   else
@@ -213,6 +482,16 @@ cudaError_t launch_ckpt_dequantize(int dtype, const int8_t* q, const uint8_t* e,
                                    const int32_t* n_rows, int rows, int src_rows, int cols, void* dst, int* status,
                                    cudaStream_t s) {
   const int nb = blocks_of(cols), grid = warp_grid(static_cast<long long>(rows) * nb);
+  if (vec_ok(cols, dst, q, nullptr, nullptr)) {
+    const Shape p = shape(rows, cols);
+    if (dtype == MOE_DTYPE_BF16)
+      ckpt_dequantize_vec_kernel<<<p.grid, 256, 0, s>>>(q, e, row_index, n_rows, rows, src_rows, cols, nb, p.lx,
+                                                        static_cast<__nv_bfloat16*>(dst), status);
+    else
+      ckpt_dequantize_vec_kernel<<<p.grid, 256, 0, s>>>(q, e, row_index, n_rows, rows, src_rows, cols, nb, p.lx,
+                                                        static_cast<float*>(dst), status);
+    return cudaGetLastError();
+  }
   if (dtype == MOE_DTYPE_BF16)
     ckpt_dequantize_kernel<<<grid, 256, 0, s>>>(q, e, row_index, n_rows, rows, src_rows, cols, nb,
                                                 static_cast<__nv_bfloat16*>(dst), status);
@@ -224,28 +503,46 @@ cudaError_t launch_ckpt_dequantize(int dtype, const int8_t* q, const uint8_t* e,
 
 namespace {
 
+template <typename TS, typename TD, bool SW>
+void run_save(const void* h, const int32_t* n_rows, int rows, int I, void* a, int8_t* q, uint8_t* e, cudaStream_t s) {
+  const int nb = blocks_of(I);
+  const TS* hp = static_cast<const TS*>(h);
+  TD* ap = static_cast<TD*>(a);
+  if (vec_ok(I, h, a, q, nullptr)) {
+    const Shape p = shape(rows, I);
+    act_save_vec_kernel<TS, TD, SW><<<p.grid, 256, 0, s>>>(hp, n_rows, rows, I, nb, p.lx, ap, q, e);
+  } else {
+    act_save_kernel<TS, TD, SW><<<warp_grid(static_cast<long long>(rows) * nb), 256, 0, s>>>(hp, n_rows, rows, I, nb,
+                                                                                             ap, q, e);
+  }
+}
 template <typename TS, typename TD>
 void run_save(bool sw, const void* h, const int32_t* n_rows, int rows, int I, void* a, int8_t* q, uint8_t* e,
               cudaStream_t s) {
-  const int nb = blocks_of(I), grid = warp_grid(static_cast<long long>(rows) * nb);
-  if (sw)
-    act_save_kernel<TS, TD, true><<<grid, 256, 0, s>>>(static_cast<const TS*>(h), n_rows, rows, I, nb,
-                                                       static_cast<TD*>(a), q, e);
-  else
-    act_save_kernel<TS, TD, false><<<grid, 256, 0, s>>>(static_cast<const TS*>(h), n_rows, rows, I, nb,
-                                                        static_cast<TD*>(a), q, e);
+  if (sw) run_save<TS, TD, true>(h, n_rows, rows, I, a, q, e, s);
+  else run_save<TS, TD, false>(h, n_rows, rows, I, a, q, e, s);
 }
 
+template <typename TS, typename TD, bool SW>
+void run_backward(const int8_t* q, const uint8_t* e, const void* da, const float* row_w, const int32_t* n_rows,
+                  int rows, int I, void* dh, void* wa, float* dw, cudaStream_t s) {
+  const int nb = blocks_of(I);
+  const TS* dp = static_cast<const TS*>(da);
+  TD* hp = static_cast<TD*>(dh);
+  TD* wp = static_cast<TD*>(wa);
+  if (vec_ok(I, q, da, dh, wa)) {
+    const Shape p = shape(rows, I);
+    act_backward_vec_kernel<TS, TD, SW><<<p.grid, 256, 0, s>>>(q, e, dp, row_w, n_rows, rows, I, nb, p.lx, hp, wp, dw);
+  } else {
+    act_backward_kernel<TS, TD, SW><<<std::min(rows, 8 * num_sms()), 256, 0, s>>>(q, e, dp, row_w, n_rows, rows, I, nb,
+                                                                                  hp, wp, dw);
+  }
+}
 template <typename TS, typename TD>
 void run_backward(bool sw, const int8_t* q, const uint8_t* e, const void* da, const float* row_w,
                   const int32_t* n_rows, int rows, int I, void* dh, void* wa, float* dw, cudaStream_t s) {
-  const int nb = blocks_of(I), grid = std::min(rows, 8 * num_sms());
-  if (sw)
-    act_backward_kernel<TS, TD, true><<<grid, 256, 0, s>>>(q, e, static_cast<const TS*>(da), row_w, n_rows, rows, I,
-                                                           nb, static_cast<TD*>(dh), static_cast<TD*>(wa), dw);
-  else
-    act_backward_kernel<TS, TD, false><<<grid, 256, 0, s>>>(q, e, static_cast<const TS*>(da), row_w, n_rows, rows, I,
-                                                            nb, static_cast<TD*>(dh), static_cast<TD*>(wa), dw);
+  if (sw) run_backward<TS, TD, true>(q, e, da, row_w, n_rows, rows, I, dh, wa, dw, s);
+  else run_backward<TS, TD, false>(q, e, da, row_w, n_rows, rows, I, dh, wa, dw, s);
 }
 
 }  // namespace
