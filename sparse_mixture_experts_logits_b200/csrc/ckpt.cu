@@ -40,45 +40,51 @@ __device__ __forceinline__ int ckpt_q(float v, float inv) {
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// sigmoid(x) and sigmoid(-x), neither by a difference: with z = exp(-|x|)
-// they are 1 / (1 + z) and z / (1 + z).  The divisor is in [1, 2], where the
-// approximate division is within 2 ulp.
-__device__ __forceinline__ void sigmoid_pair(float x, float& s, float& ns) {
-  const float z = __expf(-fabsf(x));
-  const float p = __fdividef(1.0f, 1.0f + z);
+// s = sigmoid(x) and d = s (1 - s) from y = x log2(e), without a difference:
+// with z = exp(-|x|) the larger of sigmoid(x), sigmoid(-x) is p = 1 / (1 + z)
+// and the smaller z p.  The hardware's exponential (2 ulp) and reciprocal
+// (1 ulp), with subnormal z taken as 0: the forms that keep subnormals cost
+// three instructions more for results below 2^-126.
+__device__ __forceinline__ void sigmoid_of(float y, float& s, float& d) {
+  float z, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(-fabsf(y)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + z));
   const float m = z * p;
-  s = x < 0.0f ? m : p;
-  ns = x < 0.0f ? p : m;
+  s = y < 0.0f ? m : p;
+  d = m * p;
 }
+constexpr float kLog2e = 1.4426950408889634f;
 
 // GELU (tanh form) as v sigmoid(w(v)) with w = 2 sqrt(2/pi) (v + 0.044715 v^3):
 // 0.5 (1 + tanh(w / 2)) = sigmoid(w), without the cancellation at negative v.
-// Its derivative is sigmoid(w) + v sigmoid(w) sigmoid(-w) w'(v).
+// Its derivative is sigmoid(w) + v sigmoid(w) sigmoid(-w) w'(v).  The cubic's
+// coefficients carry the log2(e) of sigmoid_of.
 constexpr float kGeluW = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluC = 0.044715f;
 __device__ __forceinline__ float gelu_sig(float v) {
-  float s, ns;
-  sigmoid_pair(kGeluW * fmaf(0.044715f * v, v * v, v), s, ns);
+  float s, d;
+  sigmoid_of(v * fmaf(kGeluW * kGeluC * kLog2e, v * v, kGeluW * kLog2e), s, d);
   return v * s;
 }
 __device__ __forceinline__ void gelu_sig_grad(float v, float& a, float& da) {
-  // beyond |v| = 20 sigmoid(-|w|) is 0 in fp32; the clamp keeps w' finite there (NaN passes through)
-  const float c = fabsf(v) > 20.0f ? copysignf(20.0f, v) : v;
-  float s, ns;
-  sigmoid_pair(kGeluW * fmaf(0.044715f * c, c * c, c), s, ns);
+  float s, d;
+  const float q = v * v;
+  sigmoid_of(v * fmaf(kGeluW * kGeluC * kLog2e, q, kGeluW * kLog2e), s, d);
   a = v * s;
-  da = fmaf(c * s * ns, kGeluW * fmaf(3.0f * 0.044715f * c, c, 1.0f), s);
+  // where v^2 overflows d is 0, and w' is kept finite so that their product is 0 too (a NaN passes through v)
+  da = fmaf(v * d, fminf(fmaf(3.0f * kGeluW * kGeluC, q, kGeluW), 3e38f), s);
 }
 __device__ __forceinline__ float swiglu(float g, float u) {
-  float s, ns;
-  sigmoid_pair(g, s, ns);
+  float s, d;
+  sigmoid_of(g * kLog2e, s, d);
   return g * s * u;
 }
 __device__ __forceinline__ void swiglu_grad(float g, float u, float& a, float& dg, float& du) {
-  float s, ns;
-  sigmoid_pair(g, s, ns);
-  du = g * s;                        // da / du = SiLU(g)
+  float s, d;
+  sigmoid_of(g * kLog2e, s, d);
+  du = g * s;               // da / du = SiLU(g)
   a = du * u;
-  dg = u * s * fmaf(g, ns, 1.0f);    // da / dg = u SiLU'(g)
+  dg = u * fmaf(g, d, s);   // da / dg = u SiLU'(g)
 }
 
 // ------------------------------------------------ any width: warp per block
@@ -196,7 +202,9 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const int8_t* __restr
 // A thread takes 8 consecutive columns, four neighbouring threads a block of
 // 32; `tx` = 2^lx threads (4 to 256) run along a row and the 256 / tx rows of a
 // thread block step through the batch together.  kU column steps are loaded
-// before any is used, which keeps 32 to 128 bytes a thread in flight.
+// before any is used, which keeps 48 to 128 bytes a thread in flight.  Results
+// go out with the streaming hint: nothing reads them again from the caches
+// before the next kernel.
 template <typename T> struct Vec8;  // 8 values as they lie in memory
 template <> struct Vec8<__nv_bfloat16> { uint4 a; };
 template <> struct Vec8<float> { float4 a, b; };
@@ -212,45 +220,90 @@ __device__ __forceinline__ void unpack8(const Vec8<float>& v, float* f) {
   f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
   f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
-  *reinterpret_cast<uint4*>(p) = f32_to_bf16x8(f);
+// Columns c .. c + 7 of a row of `cols` (every lane of the warp takes part;
+// `on`: the row exists).  fp32: 32 bytes a lane in two stores, whose halves
+// neighbouring lanes exchange so that each store fills whole 32-byte sectors.
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int c, int cols, bool on, const float* f) {
+  if (on && c < cols) __stcs(reinterpret_cast<uint4*>(row + c), f32_to_bf16x8(f));
 }
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  float4* q = reinterpret_cast<float4*>(p);
-  q[0] = make_float4(f[0], f[1], f[2], f[3]);
-  q[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* row, int c, int cols, bool on, const float* f) {
+  const bool odd = (c & 8) != 0;
+  float4 o;
+  o.x = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[4], 1);
+  o.y = __shfl_xor_sync(0xffffffffu, odd ? f[1] : f[5], 1);
+  o.z = __shfl_xor_sync(0xffffffffu, odd ? f[2] : f[6], 1);
+  o.w = __shfl_xor_sync(0xffffffffu, odd ? f[3] : f[7], 1);
+  const float4 lo = make_float4(f[0], f[1], f[2], f[3]), hi = make_float4(f[4], f[5], f[6], f[7]);
+  // even: own first half, the neighbour's first half; odd: the neighbour's second half, own second half
+  const int c0 = odd ? c - 4 : c, c1 = odd ? c + 4 : c + 8;
+  if (on && c0 < cols) __stcs(reinterpret_cast<float4*>(row + c0), odd ? o : lo);
+  if (on && c1 < cols) __stcs(reinterpret_cast<float4*>(row + c1), odd ? hi : o);
 }
 
-// q of 8 values and the exponent byte of their block (the four threads of a
-// block exchange their largest magnitudes; every lane of the warp takes part).
-__device__ __forceinline__ uint2 keep8(const float* f, uint32_t& e) {
-  uint32_t m = 0;
+// The exponent field of the largest magnitude of a thread's 8 values.  bf16:
+// on packed pairs (a NaN wins and has exponent 255, as an infinity has).
+__device__ __forceinline__ uint32_t top8(const Vec8<__nv_bfloat16>& v, const float*) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v.a);
+  const __nv_bfloat162 m =
+      __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+  const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+  return max((b >> 7) & 0xffu, (b >> 23) & 0xffu);
+}
+__device__ __forceinline__ uint32_t top8(const Vec8<float>&, const float* f) {
+  float m = 0.0f;  // max.NaN: a NaN wins
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(f[i])));
+  return (__float_as_uint(m) >> 23) & 0xffu;
+}
+
+__device__ __forceinline__ uint32_t pack4(const uint32_t* b) {
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+// q of 8 values and the exponent byte of their block (the four threads of a
+// block exchange theirs; every lane of the warp takes part).  One fused
+// multiply-add scales a value and rounds it to an integer: adding 1.5 2^23
+// leaves the integer in the last mantissa bits (the conversion instructions
+// run at an eighth of the rate).  What that does not cover is done once more
+// the long way: a value that rounds to +-128 and takes the clamp (its byte is
+// 0x80, which no other gives), a block whose scale is no fp32 number (e < 6)
+// and one that is not finite.
+template <typename T>
+__device__ __forceinline__ uint2 keep8(const Vec8<T>& v, const float* f, uint32_t& e) {
+  uint32_t m = top8(v, f);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  e = m >> 23;
-  const float inv = ckpt_inv_scale(e);
+  e = m;
+  const float scale = __uint_as_float((260u - e) << 23);
   uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(ckpt_q(f[i], inv)) & 0xffu;
-  return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(f[i], scale, 12582912.0f));
+  uint2 k = make_uint2(pack4(b), pack4(b + 4));
+  const uint32_t x = k.x ^ 0x80808080u, y = k.y ^ 0x80808080u;  // a zero byte where q is 0x80
+  const uint32_t clamped = (((x - 0x01010101u) & ~x) | ((y - 0x01010101u) & ~y)) & 0x80808080u;
+  if (clamped != 0u || e - 6u > 248u) {
+    const float inv = ckpt_inv_scale(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      b[i] = __float_as_uint(fmaf(fminf(fmaxf(f[i] * inv, -127.0f / 64.0f), 127.0f / 64.0f), 64.0f, 12582912.0f));
+    k = e == 255u ? make_uint2(0u, 0u) : make_uint2(pack4(b), pack4(b + 4));
+  }
+  return k;
 }
+// And back: the byte q + 128 under the exponent of 2^23 is 2^23 + 128 + q.
 __device__ __forceinline__ void read8(const uint2& q, uint32_t e, float* f) {
   const float s = ckpt_scale(e);
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = static_cast<float>(static_cast<int8_t>(q.x >> (8 * i))) * s;
-    f[4 + i] = static_cast<float>(static_cast<int8_t>(q.y >> (8 * i))) * s;
-  }
+  for (int i = 0; i < 8; ++i)
+    f[i] = (__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.0f) * s;
 }
 
-constexpr int kU = 2;
 
 template <typename T>
-__global__ void __launch_bounds__(256) ckpt_quantize_vec_kernel(const T* __restrict__ src, const int32_t* n_rows,
+__global__ void __launch_bounds__(256, 4) ckpt_quantize_vec_kernel(const T* __restrict__ src, const int32_t* n_rows,
                                                                 int rows, int cols, int nb, int lx,
                                                                 int8_t* __restrict__ q, uint8_t* __restrict__ e) {
+  constexpr int kU = 4;
   const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
   const int n = live_rows(n_rows, rows);
   const Vec8<T> none = {};
@@ -266,10 +319,11 @@ __global__ void __launch_bounds__(256) ckpt_quantize_vec_kernel(const T* __restr
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int c = c0 + u * 8 * tx;
+        if (c - 8 * x >= cols) break;  // behind the row for every lane
         float f[8];
         unpack8(v[u], f);
         uint32_t ex;
-        const uint2 k = keep8(f, ex);
+        const uint2 k = keep8(v[u], f, ex);
         if (r < n && c < cols) {
           *reinterpret_cast<uint2*>(q + r * cols + c) = k;
           if ((x & 3) == 0) e[r * nb + c / kBlk] = static_cast<uint8_t>(ex);
@@ -280,7 +334,7 @@ __global__ void __launch_bounds__(256) ckpt_quantize_vec_kernel(const T* __restr
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) ckpt_dequantize_vec_kernel(const int8_t* __restrict__ q,
+__global__ void __launch_bounds__(256, 4) ckpt_dequantize_vec_kernel(const int8_t* __restrict__ q,
                                                                   const uint8_t* __restrict__ e,
                                                                   const int32_t* __restrict__ row_index,
                                                                   const int32_t* n_rows, int rows, int src_rows,
@@ -289,12 +343,13 @@ __global__ void __launch_bounds__(256) ckpt_dequantize_vec_kernel(const int8_t* 
   constexpr int kD = 4;
   const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
   const int n = live_rows(n_rows, rows);
-  for (long long r = static_cast<long long>(blockIdx.x) * ny + (threadIdx.x >> lx); r < n;
-       r += static_cast<long long>(gridDim.x) * ny) {
-    const long long sr = row_index != nullptr ? row_index[r] : r;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * ny; r0 < n; r0 += static_cast<long long>(gridDim.x) * ny) {
+    const long long r = r0 + (threadIdx.x >> lx);
+    const bool live = r < n;
+    const long long sr = !live ? -1 : row_index != nullptr ? row_index[r] : r;
     const bool ok = sr >= 0 && sr < src_rows;
-    if (!ok && x == 0) set_status(status, MOE_DEVERR_BAD_ROW_TOKEN);
-    for (int c0 = 8 * x; c0 < cols; c0 += kD * 8 * tx) {
+    if (live && !ok && x == 0) set_status(status, MOE_DEVERR_BAD_ROW_TOKEN);
+    for (int c0 = 8 * x; c0 - 8 * x < cols; c0 += kD * 8 * tx) {
       uint2 k[kD];
       uint32_t ex[kD];
 #pragma unroll
@@ -307,19 +362,20 @@ __global__ void __launch_bounds__(256) ckpt_dequantize_vec_kernel(const int8_t* 
 #pragma unroll
       for (int u = 0; u < kD; ++u) {
         const int c = c0 + u * 8 * tx;
+        if (c - 8 * x >= cols) break;
         float f[8];
         read8(k[u], ex[u], f);
-        if (c < cols) store8(dst + r * cols + c, f);
+        store8(dst + r * cols, c, cols, live, f);
       }
     }
   }
 }
 
 template <typename TS, typename TD, bool SWIGLU>
-__global__ void __launch_bounds__(256) act_save_vec_kernel(const TS* __restrict__ h, const int32_t* n_rows, int rows,
+__global__ void __launch_bounds__(256, 4) act_save_vec_kernel(const TS* __restrict__ h, const int32_t* n_rows, int rows,
                                                            int I, int nb, int lx, TD* __restrict__ a,
                                                            int8_t* __restrict__ q, uint8_t* __restrict__ e) {
-  constexpr int H = SWIGLU ? 2 : 1;
+  constexpr int H = SWIGLU ? 2 : 1, kU = SWIGLU ? 2 : 4;
   const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
   const int n = live_rows(n_rows, rows);
   const Vec8<TS> none = {};
@@ -336,13 +392,14 @@ __global__ void __launch_bounds__(256) act_save_vec_kernel(const TS* __restrict_
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int c = c0 + u * 8 * tx;
+        if (c - 8 * x >= I) break;
         const bool on = r < n && c < I;
         float f[H][8], o[8];
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           unpack8(v[u][j], f[j]);
           uint32_t ex;
-          const uint2 k = keep8(f[j], ex);
+          const uint2 k = keep8(v[u][j], f[j], ex);
           if (on) {
             *reinterpret_cast<uint2*>(q + (r * H + j) * I + c) = k;
             if ((x & 3) == 0) e[(r * H + j) * nb + c / kBlk] = static_cast<uint8_t>(ex);
@@ -353,20 +410,20 @@ __global__ void __launch_bounds__(256) act_save_vec_kernel(const TS* __restrict_
           if constexpr (SWIGLU) o[i] = swiglu(f[0][i], f[1][i]);
           else o[i] = gelu_sig(f[0][i]);
         }
-        if (on) store8(a + r * I + c, o);
+        store8(a + r * I, c, I, r < n, o);
       }
     }
   }
 }
 
 template <typename TS, typename TD, bool SWIGLU>
-__global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __restrict__ q,
+__global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* __restrict__ q,
                                                                const uint8_t* __restrict__ e,
                                                                const TS* __restrict__ da,
                                                                const float* __restrict__ row_w, const int32_t* n_rows,
                                                                int rows, int I, int nb, int lx, TD* __restrict__ dh,
                                                                TD* __restrict__ wa, float* __restrict__ dw) {
-  constexpr int H = SWIGLU ? 2 : 1;
+  constexpr int H = SWIGLU ? 2 : 1, kU = SWIGLU ? 2 : 4;
   __shared__ float s_part[8];
   const int tx = 1 << lx, x = threadIdx.x & (tx - 1), ny = 256 >> lx;
   const int n = live_rows(n_rows, rows);
@@ -376,7 +433,7 @@ __global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __r
     const bool live = r < n;
     const float w = live && row_w != nullptr ? row_w[r] : 1.0f;
     float dot = 0.0f;
-    for (int c0 = 8 * x; c0 < I; c0 += kU * 8 * tx) {
+    for (int c0 = 8 * x; c0 - 8 * x < I; c0 += kU * 8 * tx) {
       uint2 k[kU][H];
       uint32_t ex[kU][H];
       Vec8<TS> v[kU];
@@ -394,7 +451,7 @@ __global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __r
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int c = c0 + u * 8 * tx;
-        const bool on = live && c < I;
+        if (c - 8 * x >= I) break;
         float g[8], f[H][8], d[H][8], o[8];
         unpack8(v[u], g);
 #pragma unroll
@@ -409,11 +466,9 @@ __global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __r
 #pragma unroll
           for (int j = 0; j < H; ++j) d[j][i] *= w * g[i];
         }
-        if (on) {
 #pragma unroll
-          for (int j = 0; j < H; ++j) store8(dh + (r * H + j) * I + c, d[j]);
-          if (wa != nullptr) store8(wa + r * I + c, o);
-        }
+        for (int j = 0; j < H; ++j) store8(dh + (r * H + j) * I, c, I, live, d[j]);
+        if (wa != nullptr) store8(wa + r * I, c, I, live, o);
       }
     }
     if (dw != nullptr) {
@@ -434,16 +489,23 @@ __global__ void __launch_bounds__(256) act_backward_vec_kernel(const int8_t* __r
   }
 }
 
-// Threads along a row (as a power of two) and the grid.  A row's threads are
-// at most one warp when there are rows enough to fill the GPU (no block-wide
-// reduction for dw, long runs per thread); few rows spread over up to 256.
+// Threads along a row (as a power of two) and the grid.  As few as one warp a
+// row where that makes 24 blocks an SM (no block-wide reduction for dw, long
+// runs per thread), up to 256 where there are fewer rows (4097 rows of 8192
+// columns: 513 blocks of one-warp rows leave the SMs unevenly filled).  Of
+// those the most that leave at most an eighth of them idle in the row's last
+// step (192 columns: 8 threads three times, not 32 of which 8 idle).
 struct Shape { int lx, grid; };
 inline Shape shape(int rows, int cols) {
-  int lx = 2;
-  const int most = rows >= 16 * num_sms() ? 5 : 8;
-  while (lx < most && (8 << lx) < cols) ++lx;
+  const int vecs = cols / 8;
+  int lx = 5;
+  while (lx < 8 && static_cast<long long>(rows) << lx < 24ll * 256 * num_sms()) ++lx;
+  for (; lx > 2; --lx) {
+    const int tx = 1 << lx, padded = (vecs + tx - 1) / tx * tx;
+    if ((padded - vecs) * 8 <= padded) break;
+  }
   const int ny = 256 >> lx;
-  return {lx, std::min((rows - 1) / ny + 1, 8 * num_sms())};
+  return {lx, std::min((rows - 1) / ny + 1, 32 * num_sms())};
 }
 inline bool vec_ok(int cols, const void* a, const void* b, const void* c, const void* d) {
   const uintptr_t any = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |

@@ -93,6 +93,9 @@ def _sig(x):
 
 
 C2 = 2 * math.sqrt(2 / math.pi)
+# exp(-|w|) below the smallest normal number may be taken as 0: that is
+# 2^-126 times whatever it is multiplied with
+TINY = 2.0 ** -126
 
 
 def act(h, swiglu):
@@ -102,10 +105,10 @@ def act(h, swiglu):
     if swiglu:
         g, u = np.split(h, 2, 1)
         a = g * _sig(g) * u
-        return a, np.abs(a) * (2.0 ** -20 + np.abs(g) * 2.0 ** -21)
+        return a, np.abs(a) * (2.0 ** -20 + np.abs(g) * 2.0 ** -21) + np.abs(g * u) * TINY
     w = C2 * (h + 0.044715 * h ** 3)
     a = h * _sig(w)
-    return a, np.abs(a) * (2.0 ** -20 + np.abs(w) * 2.0 ** -21)
+    return a, np.abs(a) * (2.0 ** -20 + np.abs(w) * 2.0 ** -21) + np.abs(h) * TINY
 
 
 def act_grad(h, swiglu):
@@ -116,7 +119,8 @@ def act_grad(h, swiglu):
         d = np.concatenate([u * s * (1 + g * n), g * s], 1)
         m = np.concatenate([np.abs(u) * s * (1 + np.abs(g) * n), np.abs(g) * s], 1)
         rel = 2.0 ** -19 + np.abs(g) * 2.0 ** -20
-        return d, m * np.concatenate([rel, rel], 1)
+        z = np.concatenate([np.abs(u) * (1 + np.abs(g)), np.abs(g)], 1) * TINY
+        return d, m * np.concatenate([rel, rel], 1) + z
     w = C2 * (h + 0.044715 * h ** 3)
     s, n, dw = _sig(w), _sig(-w), C2 * (1 + 3 * 0.044715 * h * h)
-    return s + h * s * n * dw, (s + np.abs(h) * s * n * dw) * (2.0 ** -19 + np.abs(w) * 2.0 ** -20)
+    return s + h * s * n * dw, (s + np.abs(h) * s * n * dw) * (2.0 ** -19 + np.abs(w) * 2.0 ** -20) + (1 + np.abs(h * dw)) * TINY
