@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* 
 }
 
 // Threads along a row (as a power of two) and the grid.  As few as one warp a
-// row where that makes 24 blocks an SM (no block-wide reduction for dw, long
+// row where that makes 6 blocks an SM (no block-wide reduction for dw, long
 // runs per thread), up to 256 where there are fewer rows (4097 rows of 8192
 // columns: 513 blocks of one-warp rows leave the SMs unevenly filled).  Of
 // those the most that leave at most an eighth of them idle in the row's last
@@ -499,7 +499,7 @@ struct Shape { int lx, grid; };
 inline Shape shape(int rows, int cols) {
   const int vecs = cols / 8;
   int lx = 5;
-  while (lx < 8 && static_cast<long long>(rows) << lx < 24ll * 256 * num_sms()) ++lx;
+  while (lx < 8 && static_cast<long long>(rows) << lx < 6ll * 256 * num_sms()) ++lx;
   for (; lx > 2; --lx) {
     const int tx = 1 << lx, padded = (vecs + tx - 1) / tx * tx;
     if ((padded - vecs) * 8 <= padded) break;

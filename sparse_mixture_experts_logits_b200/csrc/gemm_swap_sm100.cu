@@ -186,6 +186,7 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   a.counts = L.counts;
   a.tile_ctr = L.tile_ctr;
   a.accumulate = L.accumulate;
+  a.clear_status = L.clear_status;
   if (is_wgrad(L.layout)) {
     const long long tiles_ub = static_cast<long long>(L.num_groups) * L.w_tiles * L.b_tiles;
     if (L.layout == kSwWgradRagged) {

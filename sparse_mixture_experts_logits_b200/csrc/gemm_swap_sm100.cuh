@@ -181,6 +181,7 @@ struct SwapArgs {
   // (dynamic schedule); otherwise they take fixed rounds (swap_tile_at).
   int* tile_ctr;
   int accumulate;  // kSwWgradRagged: add onto the output
+  int clear_status;  // the first CTA clears *status at its start (nothing did before the launch)
 };
 
 // Token tiles of a segment of `cnt` rows: ceil(cnt / 256) tiles of equal
@@ -345,6 +346,10 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
   float* xbuf = reinterpret_cast<float*>(dyn_smem + (smem_base - smem_addr(dyn_smem)) + kSwStages * kSwStageBytes);
   const int G = args.num_groups;
 
+  // A call of one small launch saves the separate clear.  No error that
+  // another CTA reports can be lost to it: a wait gives up after two seconds,
+  // and every CTA of the launch is resident from the start.
+  if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0 && args.status != nullptr) *args.status = 0;
   // Segment bounds clamped to [0, rows], so that offsets that are not a
   // valid dispatch cannot send a tile outside the token buffer (a segment
   // whose end lies before its start gets no tile).

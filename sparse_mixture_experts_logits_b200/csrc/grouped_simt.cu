@@ -11,6 +11,7 @@
 // ones; all orders are fixed.
 #include <algorithm>
 
+#include "grouped_colsum.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -31,6 +32,7 @@ struct Args {
   int Kc;       // contraction length (forward, dgrad)
   int col_tiles;
   int accumulate;
+  int* status;  // cleared by the first block (nothing here sets it)
 };
 
 template <typename T, typename TO, bool WGRAD>
@@ -39,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
   __shared__ float Bs[kTK][kTN + 1];
   __shared__ int s_off[kMaxExperts + 1];
   __shared__ int s_tstart[kMaxExperts + 1];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   const T* A = static_cast<const T*>(p.A);
   const T* B = static_cast<const T*>(p.B);
   const int G = p.G;
@@ -82,17 +85,31 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
     const long long bg = static_cast<long long>(g) * p.b_gstride;
     float acc[4][4] = {}, tot[4][4] = {};
     int slices = 0;
-    for (long long k0 = c0; k0 < c1; k0 += kTK) {
-      for (int i = threadIdx.x; i < kTM * kTK; i += kThreads) {
-        // neighbouring threads read along each operand's contiguous index
-        int m, c;
+    // this thread's elements of a slice, along each operand's contiguous
+    // index; the next slice is loaded while this one is multiplied
+    constexpr int kPer = kTM * kTK / kThreads;
+    float ra[kPer], rb[kPer];
+    auto fetch = [&](long long k0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        int m, c, n, d;
         if (p.a_sc == 1) { c = i & (kTK - 1); m = i / kTK; } else { m = i & (kTM - 1); c = i / kTM; }
-        As[c][m] = (m < nm && k0 + c < c1) ? to_f32(A[(m0 + m) * p.a_sm + (k0 + c) * p.a_sc]) : 0.f;
-        int n, d;
         if (p.b_sc == 1) { d = i & (kTK - 1); n = i / kTK; } else { n = i & (kTN - 1); d = i / kTN; }
-        Bs[d][n] = (n0 + n < p.N && k0 + d < c1) ? to_f32(B[bg + (n0 + n) * p.b_sn + (k0 + d) * p.b_sc]) : 0.f;
+        ra[j] = (m < nm && k0 + c < c1) ? to_f32(A[(m0 + m) * p.a_sm + (k0 + c) * p.a_sc]) : 0.f;
+        rb[j] = (n0 + n < p.N && k0 + d < c1) ? to_f32(B[bg + (n0 + n) * p.b_sn + (k0 + d) * p.b_sc]) : 0.f;
+      }
+    };
+    fetch(c0);
+    for (long long k0 = c0; k0 < c1; k0 += kTK) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (p.a_sc == 1) As[i & (kTK - 1)][i / kTK] = ra[j]; else As[i / kTM][i & (kTM - 1)] = ra[j];
+        if (p.b_sc == 1) Bs[i & (kTK - 1)][i / kTK] = rb[j]; else Bs[i / kTN][i & (kTN - 1)] = rb[j];
       }
       __syncthreads();
+      if (k0 + kTK < c1) fetch(k0 + kTK);
 #pragma unroll
       for (int kk = 0; kk < kTK; ++kk) {
         float a[4], b[4];
@@ -133,71 +150,13 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
   }
 }
 
-// db[g, n] (+)= sum over g's rows of dy[r, n].  A block takes `share` of the
-// segment's rows (blockIdx.z) for 64 columns: its eight warps take every
-// eighth row, two columns a thread and eight rows in flight, and their sums
-// are added in warp order.  With more than one share the blocks leave partial
-// sums [share][G][N], which grouped_colsum_join_kernel adds in order.  Bound
-// by reading dy once.
-template <typename T>
-__device__ __forceinline__ float2 ld2(const T* p, bool second);
-template <>
-__device__ __forceinline__ float2 ld2(const float* p, bool second) {
-  return make_float2(p[0], second ? p[1] : 0.f);
-}
-template <>
-__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p, bool second) {
-  return make_float2(__bfloat162float(p[0]), second ? __bfloat162float(p[1]) : 0.f);
-}
-
 template <typename T, bool PAIRED>
 __global__ void __launch_bounds__(256) grouped_colsum_kernel(const T* __restrict__ dy,
                                                              const int32_t* __restrict__ offsets, int rows, int N,
                                                              int accumulate, float* __restrict__ out) {
   __shared__ float2 s[8][32];
-  const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = max(0, min(offsets[g], rows)), e = max(b, max(0, min(offsets[g + 1], rows)));
-  const int per = (e - b + gridDim.z - 1) / gridDim.z;
-  const int r0 = min(e, b + static_cast<int>(blockIdx.z) * per), r1 = min(e, r0 + per);
-  const int n = blockIdx.x * 64 + 2 * lane;
-  float2 a = make_float2(0.f, 0.f);
-  if (n < N) {
-    const bool two = n + 1 < N;
-    const T* p = dy + static_cast<long long>(r0 + warp) * N + n;
-    const long long step = 8ll * N;
-    int r = r0 + warp;
-    for (; r + 56 < r1; r += 64, p += 8 * step) {
-      float2 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (PAIRED) {  // N is even and dy on a whole pair: one load for both columns
-          if constexpr (sizeof(T) == 2)
-            v[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + i * step));
-          else
-            v[i] = *reinterpret_cast<const float2*>(p + i * step);
-        } else {
-          v[i] = ld2(p + i * step, two);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) { a.x += v[i].x; a.y += v[i].y; }
-    }
-    for (; r < r1; r += 8, p += step) {
-      const float2 v = ld2(p, two);
-      a.x += v.x;
-      a.y += v.y;
-    }
-  }
-  s[warp][lane] = a;
-  __syncthreads();
-  if (warp == 0 && n < N) {
-    float2 v = s[0][lane];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) { v.x += s[i][lane].x; v.y += s[i][lane].y; }
-    float* o = out + (static_cast<long long>(blockIdx.z) * gridDim.y + g) * N + n;
-    o[0] = accumulate ? o[0] + v.x : v.x;
-    if (n + 1 < N) o[1] = accumulate ? o[1] + v.y : v.y;
-  }
+  grouped_colsum_block<T, PAIRED>(dy, offsets, rows, N, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, accumulate,
+                                  out + (static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y) * N, s);
 }
 
 __global__ void __launch_bounds__(256) grouped_colsum_join_kernel(const float* __restrict__ part, int shares,
@@ -220,8 +179,9 @@ cudaError_t run(const Args& a, long long tiles, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s) {
+cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_t s) {
   Args a = {};
+  a.status = status;
   a.offsets = L.offsets;
   a.G = L.G;
   a.rows = L.rows;
@@ -262,26 +222,25 @@ int grouped_colsum_shares(int G, int rows, int N) {
   return static_cast<int>(std::max<long long>(1, std::min<long long>({want, most, 64})));
 }
 
-cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
-                                  int accumulate, float* db, float* part, cudaStream_t s) {
-  const int shares = grouped_colsum_shares(G, rows, N);
-  const dim3 grid((N + 63) / 64, G, shares);
-  float* out = shares > 1 ? part : db;
-  const int acc = shares > 1 ? 0 : accumulate;
-  const bool pair = N % 2 == 0 && reinterpret_cast<uintptr_t>(dy) % 8 == 0;
-  if (dtype == MOE_DTYPE_BF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(dy);
-    if (pair) grouped_colsum_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
-    else grouped_colsum_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+cudaError_t launch_grouped_colsum(const GroupedLaunch& L, cudaStream_t s) {
+  const int shares = grouped_colsum_shares(L.G, L.rows, L.N);
+  const dim3 grid((L.N + 63) / 64, L.G, shares);
+  float* out = shares > 1 ? L.part : L.db;
+  const int acc = shares > 1 ? 0 : L.accumulate;
+  const bool pair = L.N % 2 == 0 && reinterpret_cast<uintptr_t>(L.dy) % 8 == 0;
+  if (L.dtype == MOE_DTYPE_BF16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(L.dy);
+    if (pair) grouped_colsum_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
+    else grouped_colsum_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
   } else {
-    const float* p = static_cast<const float*>(dy);
-    if (pair) grouped_colsum_kernel<float, true><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
-    else grouped_colsum_kernel<float, false><<<grid, 256, 0, s>>>(p, offsets, rows, N, acc, out);
+    const float* p = static_cast<const float*>(L.dy);
+    if (pair) grouped_colsum_kernel<float, true><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
+    else grouped_colsum_kernel<float, false><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
   }
   if (shares > 1) {
-    const long long n = static_cast<long long>(G) * N;
+    const long long n = static_cast<long long>(L.G) * L.N;
     const int blocks = static_cast<int>(std::min<long long>((n + 255) / 256, 4ll * num_sms()));
-    grouped_colsum_join_kernel<<<blocks, 256, 0, s>>>(part, shares, n, accumulate, db);
+    grouped_colsum_join_kernel<<<blocks, 256, 0, s>>>(L.part, shares, n, L.accumulate, L.db);
   }
   return cudaGetLastError();
 }

@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "gemm_sm100.cuh"
+#include "grouped_colsum.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -19,13 +20,24 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // [b, e): its last (e - b) % 64 rows of src, filled up with zero rows to 64,
 // go to tail[g * 64 ..]; a group without rows gets its `out` zeroed unless it
 // is added onto.  blockIdx.x shares the 16-byte units of each; blockIdx.z
-// picks the operand.
+// picks the operand.  Blocks of blockIdx.z = 2 take db's column sums when
+// they fit one block per 64 columns and group (a launch saved), and the first
+// block clears the status word.
 __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restrict__ x, const uint4* __restrict__ dy,
                                                             const int32_t* __restrict__ offsets, int rows, int vk,
                                                             int vn, long long out_units, int accumulate,
                                                             uint4* __restrict__ x_tail, uint4* __restrict__ dy_tail,
-                                                            uint4* __restrict__ out) {
+                                                            uint4* __restrict__ out, float* __restrict__ db,
+                                                            int* status) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
   const int g = blockIdx.y;
+  if (blockIdx.z == 2) {
+    __shared__ float2 part[8][32];
+    for (int nt = blockIdx.x; nt * 64 < 8 * vn; nt += gridDim.x)
+      grouped_colsum_block<__nv_bfloat16, true>(reinterpret_cast<const __nv_bfloat16*>(dy), offsets, rows, 8 * vn, nt,
+                                                g, 0, 1, accumulate, db + static_cast<long long>(g) * 8 * vn, part);
+    return;
+  }
   const int b = max(0, min(offsets[g], rows)), e = max(0, min(offsets[g + 1], rows));
   const int tid = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -71,11 +83,17 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     const long long units = static_cast<long long>(L.N) * L.K / 4;
     const long long most = std::max<long long>(kTail * static_cast<long long>(std::max(vk, vn)), units / 2);
     const int share = static_cast<int>(std::max<long long>(1, std::min<long long>((most + 1023) / 1024, 32)));
-    wgrad_prepare_kernel<<<dim3(share, L.G, 2), 256, 0, s>>>(
+    const bool sums = L.db != nullptr && grouped_colsum_shares(L.G, L.rows, L.N) == 1;
+    wgrad_prepare_kernel<<<dim3(share, L.G, sums ? 3 : 2), 256, 0, s>>>(
         static_cast<const uint4*>(L.x), static_cast<const uint4*>(L.dy), L.offsets, L.rows, vk, vn, units,
-        L.accumulate, reinterpret_cast<uint4*>(x_tail), reinterpret_cast<uint4*>(dy_tail), static_cast<uint4*>(L.out));
+        L.accumulate, reinterpret_cast<uint4*>(x_tail), reinterpret_cast<uint4*>(dy_tail), static_cast<uint4*>(L.out),
+        L.db, reinterpret_cast<int*>(base));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (L.db != nullptr && !sums) {
+      e = launch_grouped_colsum(L, s);
+      if (e != cudaSuccess) return e;
+    }
     // A = x (the output's contiguous index), B = dy: dw[g][n][k]
     S.epi = EPI_OUT_F32;
     S.layout = kSwWgradRagged;
@@ -90,7 +108,18 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     return launch_gemm_swap(S, s);
   }
   S.W = L.w; S.w_rows = wrows;
-  S.tile_ctr = reinterpret_cast<int*>(base) + 2;
+  // The tile counter balances what follows a CTA pair's first tile: a launch
+  // that gives each pair one at most goes without it, and without the clear
+  // of the counter (and of the status word) in a launch of its own.
+  const int out_cols = L.dir == kGroupedDgrad ? L.K : L.N;
+  const long long tiles = (L.rows / 256 + std::min(L.G, L.rows)) * static_cast<long long>((out_cols + 255) / 256);
+  if (2 * tiles <= num_sms()) {
+    S.clear_status = 1;
+  } else {
+    S.tile_ctr = reinterpret_cast<int*>(base) + 2;
+    const cudaError_t e = cudaMemsetAsync(base, 0, 16, s);
+    if (e != cudaSuccess) return e;
+  }
   if (L.dir == kGroupedDgrad) {
     S.layout = kSwDgrad;
     S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;

@@ -104,6 +104,7 @@ struct SwapLaunch {
   // [G * 64, b_cols]), and whether the output is added onto
   const void* W_tail; const void* X_tail;
   int accumulate;
+  int clear_status;          // clear *status in the launch itself
 };
 cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s);
 
@@ -122,20 +123,21 @@ struct GroupedLaunch {
   const void* bias;        // [G, N] or null
   int accumulate;          // wgrad: add onto out
   void* out;
+  // wgrad: the bias gradient db [G, N] (fp32, or null) and, when
+  // grouped_colsum_shares(...) > 1, that many [G, N] of partial sums
+  float* db;
+  float* part;
 };
-cudaError_t launch_grouped_simt(const GroupedLaunch& L, cudaStream_t s);
+cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_t s);
 // grouped_tc.cu: the same products of bf16 operands on the tensor cores (N and
 // K multiples of 8, tensors on 16-byte boundaries).  `ws` holds
-// grouped_tc_workspace(dir, G, N, K) bytes, its first 16 cleared before the call: the status
-// word and two tile counters.
+// grouped_tc_workspace(dir, G, N, K) bytes, the status word first.
 bool grouped_tc_ok(int dtype, int N, int K);
 size_t grouped_tc_workspace(int dir, int G, int N, int K);
 cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s);
-// db [G, N] (fp32) (+)= column sums of dy over each segment.  `part` holds
-// grouped_colsum_shares(...) * G * N floats when that is more than one share.
+// L.db (+)= column sums of dy over each segment.
 int grouped_colsum_shares(int G, int rows, int N);
-cudaError_t launch_grouped_colsum(int dtype, const void* dy, const int32_t* offsets, int G, int rows, int N,
-                                  int accumulate, float* db, float* part, cudaStream_t s);
+cudaError_t launch_grouped_colsum(const GroupedLaunch& L, cudaStream_t s);
 
 // ckpt.cu: activation checkpoints in 8 bits (blocks of MOE_CKPT_BLOCK columns).
 cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,

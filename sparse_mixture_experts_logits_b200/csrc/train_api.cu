@@ -38,9 +38,11 @@ WgradWs wgrad_layout(int G, int N, int K, int rows, int dtype) {
   return L;
 }
 
+// Clears the status word first (in the launches themselves).
 moe_status_t run_grouped(const GroupedLaunch& L, void* ws, cudaStream_t s) {
-  MOE_CUDA(cudaMemsetAsync(ws, 0, 16, s));
-  return cuda_status(grouped_tc_ok(L.dtype, L.N, L.K) ? launch_grouped_tc(L, ws, s) : launch_grouped_simt(L, s));
+  if (grouped_tc_ok(L.dtype, L.N, L.K)) return cuda_status(launch_grouped_tc(L, ws, s));
+  MOE_CUDA(launch_grouped_simt(L, static_cast<int*>(ws), s));
+  return L.db != nullptr ? cuda_status(launch_grouped_colsum(L, s)) : MOE_OK;
 }
 
 // The arguments that the two row products share.
@@ -127,9 +129,9 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
   L.offsets = offsets;
   L.x = x; L.dy = dy; L.out = dw;
   L.accumulate = accumulate != 0;
-  MOE_TRY(run_grouped(L, ws, s));
-  if (db) MOE_CUDA(launch_grouped_colsum(dtype, dy, offsets, G, rows, N, accumulate != 0, db, at<float*>(ws, W.part), s));
-  return MOE_OK;
+  L.db = db;
+  L.part = at<float*>(ws, W.part);
+  return run_grouped(L, ws, s);
 }
 
 int moe_ckpt_blocks(int cols) { return cols < 1 ? 0 : (cols - 1) / MOE_CKPT_BLOCK + 1; }

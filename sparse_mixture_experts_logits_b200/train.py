@@ -41,7 +41,7 @@ class _Handle:
 
     def _in(self, name, t, shape, dtype):
         """t's address; t must be a contiguous [shape] tensor of dtype on the handle's device."""
-        if t.dtype is not dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.device}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
@@ -64,7 +64,7 @@ class _Handle:
 
     def _stream(self, stream):
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
         return stream.cuda_stream
