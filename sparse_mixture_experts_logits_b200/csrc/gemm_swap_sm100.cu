@@ -40,15 +40,15 @@ bool tmap_bf16(CUtensorMap* map, const void* base, long long rows, int cols, int
 }
 
 // fp32 [groups][rows][cols] with row pitch `ld` and group pitch `gstride`
-// elements, boxes of 32 columns x box_rows rows, no swizzle: the weight-gradient output.
+// elements, boxes of box_cols columns x box_rows rows, no swizzle: the weight-gradient output.
 bool tmap_f32_out(CUtensorMap* map, void* base, int cols, long long rows, int groups, long long ld,
-                  long long gstride, int box_rows) {
+                  long long gstride, int box_cols, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(groups)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 4, static_cast<cuuint64_t>(gstride) * 4};
-  cuuint32_t box[3] = {32, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
@@ -147,7 +147,7 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
     if (L.num_groups > 1 && L.out_gstride < static_cast<long long>(L.b_cols) * L.ldo) return cudaErrorInvalidValue;
     if (!tmap_f32_out(&m.out, L.out, L.out_cols, L.b_cols, L.num_groups, L.ldo,
                       L.num_groups > 1 ? L.out_gstride : static_cast<long long>(L.b_cols) * L.ldo,
-                      L.layout == kSwWgradRagged ? kSwRgBufRows : 32))
+                      L.layout == kSwWgradRagged ? 128 : 32, L.layout == kSwWgradRagged ? kSwRgBufRows : 32))
       return cudaErrorInvalidValue;
   } else {
     for (int i = 0; i < kSwBoxes; ++i)

@@ -82,20 +82,23 @@ constexpr int kSwDynSmem = kSwStages * kSwStageBytes + kSwXBytes + 1024;
 constexpr int kSwMaxTile = 256;               // tokens per tile
 
 // kSwWgradRagged's stages: five of one k-block (32 KB), and the rest of the
-// shared memory as three 2 KB store-staging buffers per epilogue warp.  An
-// expert's contraction is short (a few k-blocks a tile), so the loads of the
-// next tile have to be in flight while the last one is stored: with two
-// stages of two k-blocks its tiles waited for their loads.
+// shared memory as three 8 KB store-staging buffers for each half of the
+// epilogue warps.  An expert's contraction is short (a few k-blocks a tile),
+// so the loads of the next tile have to be in flight while the last one is
+// stored: with two stages of two k-blocks its tiles waited for their loads.
+// The four warps that share a half fill one 16-row buffer together, so that a
+// store's rows are 512 bytes long: the copy engine works row by row, and loads
+// and stores of 128-byte rows (a buffer per warp) kept it busy most of a tile.
 constexpr int kSwRgStages = 5;
 constexpr int kSwPrefetchKb = 6;
-constexpr int kSwRgBufs = 3;
+constexpr int kSwRgBufs = 3;  // see the barrier count in the epilogue before changing
 constexpr int kSwRgBufRows = 16;
-constexpr int kSwRgBufBytes = kSwRgBufRows * 32 * 4;
+constexpr int kSwRgBufBytes = kSwRgBufRows * 128 * 4;
 template <int LAYOUT>
 constexpr int swap_kb() { return LAYOUT == kSwWgradRagged ? 1 : kSwKB; }
 template <int LAYOUT>
 constexpr int swap_stage_bytes() { return swap_kb<LAYOUT>() * (kSwATileBytes + kSwBTileBytes); }
-static_assert(kSwRgStages * swap_stage_bytes<kSwWgradRagged>() + 8 * kSwRgBufs * kSwRgBufBytes + 1024 <= kSwDynSmem,
+static_assert(kSwRgStages * swap_stage_bytes<kSwWgradRagged>() + 2 * kSwRgBufs * kSwRgBufBytes + 1024 <= kSwDynSmem,
               "the ragged weight gradient's buffers fit the launch's shared memory");
 static_assert(kBK == 64, "the MMA loop issues four K = 16 slices per stage");
 
@@ -738,8 +741,8 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           tc_fence_before();
           mbar_arrive_remote(cb ? tempty1 : tempty0);
         }
-        if (!ok) break;
         if constexpr (!kWgrad) {
+          if (!ok) break;
           const size_t ld = args.ldo;
 #pragma unroll
           for (int j = 0; j < kPieces; ++j) {
@@ -751,33 +754,40 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
               if (i < nv) *op = sum[j][i] + bias;
           }
         } else {
-          // staged in the output's own layout (lane = column) and sent out by
-          // TMA, 16 output rows a box; the tensor map clips rows past b_cols
-          // and columns past out_cols.  A tile that is added onto is added by
-          // the store itself (one add per element and launch).
-          const int col0 = col - lane;
-          const uint32_t rbuf = smem_base + S * kStage + (warp - 2) * kSwRgBufs * kSwRgBufBytes;
+          // Staged in the output's own layout by the four warps of this half
+          // and sent out by TMA, 16 output rows of 128 columns a box; the
+          // tensor map clips rows past b_cols and columns past out_cols.  A
+          // tile that is added onto is added by the store itself (one add per
+          // element and launch).  The half first agrees that none of its
+          // warps gave up a wait: the barriers below expect all four.
+          if (!named_barrier_and(1 + part, 128, ok)) { ok = false; break; }
+          const int col0 = t.wt * args.cols_per_tile + static_cast<int>(rank) * 128;
+          const uint32_t rbuf = smem_base + S * kStage + part * kSwRgBufs * kSwRgBufBytes;
           float* rbufp = reinterpret_cast<float*>(dyn_smem + (rbuf - smem_addr(dyn_smem)));
+          if (col0 < args.out_cols) {
 #pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
+            for (int j = 0; j < kPieces; ++j) {
 #pragma unroll
-            for (int h = 0; h < 32; h += kSwRgBufRows) {
-              const int c = 32 * (part + kParts * j) + h;
-              if (col0 < args.out_cols && c < t.nrows) {
-                if (lane == 0) bulk_wait_group_read<kSwRgBufs - 1>();  // buffer sc's last store has read it
-                __syncwarp();
-                float* st = rbufp + sc * (kSwRgBufBytes / 4);
+              for (int h = 0; h < 32; h += kSwRgBufRows) {
+                const int c = 32 * (part + kParts * j) + h;
+                if (c < t.nrows) {
+                  // Buffer sc is free: its last store is three boxes back, and
+                  // the storing thread saw that one read before it came to the
+                  // barrier of the box before this one.
+                  float* st = rbufp + sc * (kSwRgBufBytes / 4) + q * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < kSwRgBufRows; ++i) st[i * 32 + lane] = sum[j][h + i];
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  const uint32_t src = rbuf + sc * kSwRgBufBytes;
-                  if (args.accumulate) tma_reduce_add_3d(&maps.out, src, col0, t.tok0 + c, t.g);
-                  else tma_store_3d(&maps.out, src, col0, t.tok0 + c, t.g);
-                  bulk_commit_group();
+                  for (int i = 0; i < kSwRgBufRows; ++i) st[i * 128] = sum[j][h + i];
+                  fence_proxy_async_smem();
+                  named_barrier_sync(1 + part, 128);
+                  if (q == 0 && lane == 0) {
+                    const uint32_t src = rbuf + sc * kSwRgBufBytes;
+                    if (args.accumulate) tma_reduce_add_3d(&maps.out, src, col0, t.tok0 + c, t.g);
+                    else tma_store_3d(&maps.out, src, col0, t.tok0 + c, t.g);
+                    bulk_commit_group();
+                    bulk_wait_group_read<1>();
+                  }
+                  sc = sc + 1 == kSwRgBufs ? 0 : sc + 1;
                 }
-                sc = sc + 1 == kSwRgBufs ? 0 : sc + 1;
               }
             }
           }
