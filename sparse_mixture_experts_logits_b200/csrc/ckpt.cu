@@ -40,18 +40,48 @@ __device__ __forceinline__ int ckpt_q(float v, float inv) {
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// Two fp32 values in one register pair: one instruction for both (the
+// activations are otherwise bound by instruction issue beside the memory).
+struct F2 { unsigned long long v; };
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void un2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // s = sigmoid(x) and d = s (1 - s) from y = x log2(e), without a difference:
-// with z = exp(-|x|) the larger of sigmoid(x), sigmoid(-x) is p = 1 / (1 + z)
-// and the smaller z p.  The hardware's exponential (2 ulp) and reciprocal
-// (1 ulp), with subnormal z taken as 0: the forms that keep subnormals cost
-// three instructions more for results below 2^-126.
-__device__ __forceinline__ void sigmoid_of(float y, float& s, float& d) {
-  float z, p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(-fabsf(y)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + z));
-  const float m = z * p;
-  s = y < 0.0f ? m : p;
-  d = m * p;
+// with z = exp(-x) they are s = 1 / (1 + z) and (z s) s.  The hardware's
+// exponential (2 ulp) and reciprocal (1 ulp, 0 instead of a subnormal); the
+// clamp at y = -127 keeps z finite where s is 0.  (A NaN is clamped too: it
+// reaches the results through the factors x.)
+__device__ __forceinline__ void sigmoid_of(F2 y, F2& s, F2& d) {
+  float y0, y1, z0, z1, p0, p1;
+  un2(y, y0, y1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z0) : "f"(-fmaxf(y0, -127.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z1) : "f"(-fmaxf(y1, -127.0f)));
+  const F2 z = f2(z0, z1);
+  un2(z + f2(1.0f), p0, p1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(p0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(p1));
+  s = f2(p0, p1);
+  d = z * s * s;
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -61,30 +91,32 @@ constexpr float kLog2e = 1.4426950408889634f;
 // coefficients carry the log2(e) of sigmoid_of.
 constexpr float kGeluW = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluC = 0.044715f;
-__device__ __forceinline__ float gelu_sig(float v) {
-  float s, d;
-  sigmoid_of(v * fmaf(kGeluW * kGeluC * kLog2e, v * v, kGeluW * kLog2e), s, d);
+__device__ __forceinline__ F2 gelu_sig(F2 v) {
+  F2 s, d;
+  sigmoid_of(v * fma2(f2(kGeluW * kGeluC * kLog2e), v * v, f2(kGeluW * kLog2e)), s, d);
   return v * s;
 }
-__device__ __forceinline__ void gelu_sig_grad(float v, float& a, float& da) {
-  float s, d;
-  const float q = v * v;
-  sigmoid_of(v * fmaf(kGeluW * kGeluC * kLog2e, q, kGeluW * kLog2e), s, d);
+__device__ __forceinline__ void gelu_sig_grad(F2 v, F2& a, F2& da) {
+  F2 s, d;
+  const F2 q = v * v;
+  sigmoid_of(v * fma2(f2(kGeluW * kGeluC * kLog2e), q, f2(kGeluW * kLog2e)), s, d);
   a = v * s;
-  // where v^2 overflows d is 0, and w' is kept finite so that their product is 0 too (a NaN passes through v)
-  da = fmaf(v * d, fminf(fmaf(3.0f * kGeluW * kGeluC, q, kGeluW), 3e38f), s);
+  // w' is kept finite where v^2 overflows: d is next to 0 there
+  float w0, w1;
+  un2(fma2(f2(3.0f * kGeluW * kGeluC), q, f2(kGeluW)), w0, w1);
+  da = fma2(v * d, f2(fminf(w0, 1e18f), fminf(w1, 1e18f)), s);
 }
-__device__ __forceinline__ float swiglu(float g, float u) {
-  float s, d;
-  sigmoid_of(g * kLog2e, s, d);
+__device__ __forceinline__ F2 swiglu(F2 g, F2 u) {
+  F2 s, d;
+  sigmoid_of(g * f2(kLog2e), s, d);
   return g * s * u;
 }
-__device__ __forceinline__ void swiglu_grad(float g, float u, float& a, float& dg, float& du) {
-  float s, d;
-  sigmoid_of(g * kLog2e, s, d);
-  du = g * s;               // da / du = SiLU(g)
+__device__ __forceinline__ void swiglu_grad(F2 g, F2 u, F2& a, F2& dg, F2& du) {
+  F2 s, d;
+  sigmoid_of(g * f2(kLog2e), s, d);
+  du = g * s;                // da / du = SiLU(g)
   a = du * u;
-  dg = u * fmaf(g, d, s);   // da / dg = u SiLU'(g)
+  dg = u * fma2(g, d, s);    // da / dg = u SiLU'(g)
 }
 
 // ------------------------------------------------ any width: warp per block
@@ -151,8 +183,10 @@ __global__ void __launch_bounds__(256) act_save_kernel(const TS* __restrict__ h,
       if (lane == 0) e[(r * H + j) * nb + b] = static_cast<uint8_t>(ex);
     }
     if (c < I) {
-      if constexpr (SWIGLU) a[r * I + c] = from_f32<TD>(swiglu(v[0], v[1]));
-      else a[r * I + c] = from_f32<TD>(gelu_sig(v[0]));
+      float o, unused;
+      if constexpr (SWIGLU) un2(swiglu(f2(v[0]), f2(v[1])), o, unused);
+      else un2(gelu_sig(f2(v[0])), o, unused);
+      a[r * I + c] = from_f32<TD>(o);
     }
   }
 }
@@ -176,8 +210,13 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const int8_t* __restr
 #pragma unroll
       for (int j = 0; j < H; ++j)
         v[j] = static_cast<float>(q[(r * H + j) * I + c]) * ckpt_scale(e[(r * H + j) * nb + c / kBlk]);
-      if constexpr (SWIGLU) swiglu_grad(v[0], v[1], a, d[0], d[1]);
-      else gelu_sig_grad(v[0], a, d[0]);
+      F2 a2, d2[2];
+      float unused;
+      if constexpr (SWIGLU) swiglu_grad(f2(v[0]), f2(v[1]), a2, d2[0], d2[1]);
+      else gelu_sig_grad(f2(v[0]), a2, d2[0]);
+      un2(a2, a, unused);
+#pragma unroll
+      for (int j = 0; j < H; ++j) un2(d2[j], d[j], unused);
 #pragma unroll
       for (int j = 0; j < H; ++j) dh[(r * H + j) * I + c] = from_f32<TD>(w * g * d[j]);
       if (wa != nullptr) wa[r * I + c] = from_f32<TD>(w * a);
@@ -291,11 +330,11 @@ __device__ __forceinline__ uint2 keep8(const Vec8<T>& v, const float* f, uint32_
 }
 // And back: the byte q + 128 under the exponent of 2^23 is 2^23 + 128 + q.
 __device__ __forceinline__ void read8(const uint2& q, uint32_t e, float* f) {
-  const float s = ckpt_scale(e);
+  const F2 s = f2(ckpt_scale(e));
   const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  auto byte = [&](int i) { return __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3))); };
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    f[i] = (__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.0f) * s;
+  for (int i = 0; i < 8; i += 2) un2((f2(byte(i), byte(i + 1)) + f2(-8388736.0f)) * s, f[i], f[i + 1]);
 }
 
 
@@ -406,9 +445,10 @@ __global__ void __launch_bounds__(256, 4) act_save_vec_kernel(const TS* __restri
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (SWIGLU) o[i] = swiglu(f[0][i], f[1][i]);
-          else o[i] = gelu_sig(f[0][i]);
+        for (int i = 0; i < 8; i += 2) {
+          const F2 h0 = f2(f[0][i], f[0][i + 1]);
+          if constexpr (SWIGLU) un2(swiglu(h0, f2(f[H - 1][i], f[H - 1][i + 1])), o[i], o[i + 1]);
+          else un2(gelu_sig(h0), o[i], o[i + 1]);
         }
         store8(a + r * I, c, I, r < n, o);
       }
@@ -431,8 +471,8 @@ __global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* 
   for (long long r0 = static_cast<long long>(blockIdx.x) * ny; r0 < n; r0 += static_cast<long long>(gridDim.x) * ny) {
     const long long r = r0 + (threadIdx.x >> lx);
     const bool live = r < n;
-    const float w = live && row_w != nullptr ? row_w[r] : 1.0f;
-    float dot = 0.0f;
+    const F2 w2 = f2(live && row_w != nullptr ? row_w[r] : 1.0f);
+    F2 dot2 = f2(0.0f);
     for (int c0 = 8 * x; c0 - 8 * x < I; c0 += kU * 8 * tx) {
       uint2 k[kU][H];
       uint32_t ex[kU][H];
@@ -457,14 +497,16 @@ __global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* 
 #pragma unroll
         for (int j = 0; j < H; ++j) read8(k[u][j], ex[u][j], f[j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float act;
-          if constexpr (SWIGLU) swiglu_grad(f[0][i], f[1][i], act, d[0][i], d[1][i]);
-          else gelu_sig_grad(f[0][i], act, d[0][i]);
-          dot = fmaf(g[i], act, dot);
-          o[i] = w * act;
+        for (int i = 0; i < 8; i += 2) {
+          const F2 h0 = f2(f[0][i], f[0][i + 1]), gi = f2(g[i], g[i + 1]);
+          F2 act, di[2];
+          if constexpr (SWIGLU) swiglu_grad(h0, f2(f[H - 1][i], f[H - 1][i + 1]), act, di[0], di[1]);
+          else gelu_sig_grad(h0, act, di[0]);
+          dot2 = fma2(gi, act, dot2);
+          un2(w2 * act, o[i], o[i + 1]);
+          const F2 wg = w2 * gi;
 #pragma unroll
-          for (int j = 0; j < H; ++j) d[j][i] *= w * g[i];
+          for (int j = 0; j < H; ++j) un2(di[j] * wg, d[j][i], d[j][i + 1]);
         }
 #pragma unroll
         for (int j = 0; j < H; ++j) store8(dh + (r * H + j) * I, c, I, live, d[j]);
@@ -474,6 +516,9 @@ __global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* 
     if (dw != nullptr) {
       // a row's threads are one aligned part of a warp, or whole warps: the
       // sum runs over the part, then over the warps in order
+      float dot, dot1;
+      un2(dot2, dot, dot1);
+      dot += dot1;
       for (int o = min(tx, 32) >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if (tx > 32) {
         if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dot;
