@@ -474,6 +474,48 @@ moe_status_t moe_backward(const moe_layer_desc_t* d, const moe_weights_t* w, con
 /* Number of kernels one moe_backward call with this descriptor launches. */
 int moe_backward_launch_count(const moe_layer_desc_t* d);
 
+/* ---- training with an 8-bit checkpoint ---------------------------------
+ * moe_backward recomputes the routing and every pre-activation from x.  Here
+ * the forward keeps them instead: the pre-activations in 8 bits (the format
+ * below; routed rows in dispatch order, then the shared expert's), one byte
+ * and 1/32 per value, with the routing (indices, weights, logits).  The
+ * backward then runs no router, no top-k (so no other choice at a near-tie)
+ * and no up projection: for a SwiGLU layer 6 of moe_backward's 8 units of
+ * matrix work, and none of its fp32 pre-activations.  Its gradients are those
+ * of the kept values: act', and the activations that feed dw2 and the gate
+ * weights' gradient, are taken at h' with |h' - h| < 1/64 of the largest
+ * magnitude in h's block of 32. */
+
+/* Bytes of a checkpoint (256-byte aligned, caller-owned); 0 if the descriptor
+ * is invalid. */
+size_t moe_checkpoint_size(const moe_layer_desc_t* d);
+
+/* Byte offsets of a checkpoint's parts, into out[MOE_CHECKPOINT_PARTS]:
+ *   0 topk_idx int32 [T, k]   1 topk_w fp32 [T, k]   2 logits fp32 [T, M]
+ *   3 q, 4 e: the routed experts' pre-activations as moe_act_save lays them
+ *     out, T k rows in dispatch order, width I
+ *   5 q, 6 e: the shared expert's, T rows, width I_sh (nothing if I_sh = 0) */
+#define MOE_CHECKPOINT_PARTS 7
+moe_status_t moe_checkpoint_offsets(const moe_layer_desc_t* d, size_t* out);
+size_t moe_forward_save_workspace_size(const moe_layer_desc_t* d);
+
+/* moe_forward (addend NULL) or moe_forward_add, also writing the checkpoint.
+ * bf16: the same y bit for bit, except at decode sizes, which take the same
+ * path as larger ones here; fp32: the activation is evaluated apart from the
+ * product and rounds by itself.  topk_idx and topk_w go to the checkpoint,
+ * not to the workspace. */
+moe_status_t moe_forward_save(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x,
+                              const void* addend, void* y, void* ckpt, size_t ckpt_bytes,
+                              void* ws, size_t ws_bytes, void* stream);
+
+size_t moe_backward_saved_workspace_size(const moe_layer_desc_t* d);
+
+/* moe_backward from the checkpoint that moe_forward_save wrote for the same
+ * descriptor, weights and x.  ckpt is only read.  Errors as moe_backward. */
+moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x,
+                                const void* dy, const void* ckpt, size_t ckpt_bytes,
+                                const moe_grads_t* grads, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- matrix products grouped by expert ----------------------------------
  * The products that moe_expert_ffn and moe_backward fuse with their
  * activations, one by one: for an expert of another form, an optimizer's own

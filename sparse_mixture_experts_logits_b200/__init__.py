@@ -23,8 +23,10 @@ from .abi import (  # noqa: F401
     moe_grouped_workspace_size, moe_grouped_gemm, moe_grouped_dgrad,
     moe_grouped_wgrad_workspace_size, moe_grouped_wgrad,
     moe_ckpt_blocks, moe_ckpt_quantize, moe_ckpt_dequantize, moe_act_save, moe_act_backward, CKPT_BLOCK,
+    moe_checkpoint_size, moe_checkpoint_offsets, CHECKPOINT_PARTS, moe_forward_save_workspace_size, moe_forward_save,
+    moe_backward_saved_workspace_size, moe_backward_saved,
     DTYPE_F32, DTYPE_BF16, GATE_SOFTMAX, GATE_SIGMOID_BIAS, ACT_GELU_TANH, ACT_SWIGLU,
     DEVERR_NONE, DEVERR_BAD_EXPERT_INDEX, DEVERR_TIMEOUT, DEVERR_BAD_ROW_TOKEN, DEVERR_BAD_COUNT,
 )
-from .layer import DenseLayer, MoELayer, dense_desc_from_config, desc_from_config, weights_from_tensors  # noqa: F401,E501
+from .layer import DenseLayer, LayerCheckpoint, MoELayer, dense_desc_from_config, desc_from_config, weights_from_tensors  # noqa: F401,E501
 from .train import ActivationCheckpoint, GroupedLinear, RowCheckpoint  # noqa: F401

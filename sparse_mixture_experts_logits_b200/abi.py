@@ -32,8 +32,11 @@ EXPORTED_SYMBOLS = [
     "moe_grouped_workspace_size", "moe_grouped_gemm", "moe_grouped_dgrad",
     "moe_grouped_wgrad_workspace_size", "moe_grouped_wgrad",
     "moe_ckpt_blocks", "moe_ckpt_quantize", "moe_ckpt_dequantize", "moe_act_save", "moe_act_backward",
+    "moe_checkpoint_size", "moe_checkpoint_offsets", "moe_forward_save_workspace_size", "moe_forward_save",
+    "moe_backward_saved_workspace_size", "moe_backward_saved",
 ]
 CKPT_BLOCK = 32
+CHECKPOINT_PARTS = 7
 NUM_STAGE_EVENTS = 9
 NUM_DENSE_EVENTS = 3
 STAGE_NAMES = ["route", "dispatch", "gather", "expert_up", "expert_down", "shared_up", "shared_down",
@@ -142,6 +145,13 @@ _decl("moe_ckpt_quantize", _i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp])
 _decl("moe_ckpt_dequantize", _i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp])
 _decl("moe_act_save", _i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp])
 _decl("moe_act_backward", _i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp])
+
+_decl("moe_checkpoint_size", _sz, [_P(LayerDesc)])
+_decl("moe_checkpoint_offsets", _i, [_P(LayerDesc), _P(_sz)])
+_decl("moe_forward_save_workspace_size", _sz, [_P(LayerDesc)])
+_decl("moe_forward_save", _i, [_P(LayerDesc), _P(Weights), _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp])
+_decl("moe_backward_saved_workspace_size", _sz, [_P(LayerDesc)])
+_decl("moe_backward_saved", _i, [_P(LayerDesc), _P(Weights), _vp, _vp, _vp, _sz, _P(Grads), _vp, _sz, _vp])
 
 
 def _status_name(s: int) -> str:
@@ -364,3 +374,31 @@ def moe_act_save(h, n_rows, rows, I, act, dtype, src_dtype, a, q, e, stream=None
 def moe_act_backward(q, e, da, row_w, n_rows, rows, I, act, dtype, src_dtype, dh, wa=None, dw=None, stream=None):
     _check("moe_act_backward", lib.moe_act_backward(q, e, da, row_w, n_rows, rows, I, act, dtype, src_dtype, dh, wa,
                                                     dw, stream))
+
+
+def moe_checkpoint_size(desc: LayerDesc) -> int:
+    return lib.moe_checkpoint_size(ctypes.byref(desc))
+
+
+def moe_checkpoint_offsets(desc: LayerDesc) -> list:
+    out = (ctypes.c_size_t * CHECKPOINT_PARTS)()
+    _check("moe_checkpoint_offsets", lib.moe_checkpoint_offsets(ctypes.byref(desc), out))
+    return list(out)
+
+
+def moe_forward_save_workspace_size(desc: LayerDesc) -> int:
+    return lib.moe_forward_save_workspace_size(ctypes.byref(desc))
+
+
+def moe_forward_save(desc, weights, x, addend, y, ckpt, ckpt_bytes, ws, ws_bytes, stream=None):
+    _check("moe_forward_save", lib.moe_forward_save(ctypes.byref(desc), ctypes.byref(weights), x, addend, y, ckpt,
+                                                    ckpt_bytes, ws, ws_bytes, stream))
+
+
+def moe_backward_saved_workspace_size(desc: LayerDesc) -> int:
+    return lib.moe_backward_saved_workspace_size(ctypes.byref(desc))
+
+
+def moe_backward_saved(desc, weights, x, dy, ckpt, ckpt_bytes, grads, ws, ws_bytes, stream=None):
+    _check("moe_backward_saved", lib.moe_backward_saved(
+        ctypes.byref(desc), ctypes.byref(weights), x, dy, ckpt, ckpt_bytes, ctypes.byref(grads), ws, ws_bytes, stream))

@@ -16,29 +16,15 @@
 // and written once per form (bf16 or fp32 in, 8 bits + 1/32 byte out).
 #include <algorithm>
 
+#include "ckpt.cuh"
 #include "kernels.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBlk = MOE_CKPT_BLOCK;
-
 __device__ __forceinline__ int live_rows(const int32_t* n_rows, int rows) {
   return n_rows != nullptr ? max(0, min(rows, *n_rows)) : rows;
 }
-
-// 2^(127 - E): takes the block's largest magnitude into [1, 2).  E = 255: 0.
-__device__ __forceinline__ float ckpt_inv_scale(uint32_t e) {
-  return __uint_as_float(e < 254u ? (254u - e) << 23 : (e == 254u ? 0x00400000u : 0u));
-}
-// 2^(E - 133), subnormal for E <= 6; E = 255: NaN.
-__device__ __forceinline__ float ckpt_scale(uint32_t e) {
-  return __uint_as_float(e >= 255u ? 0x7fc00000u : (e >= 7u ? (e - 6u) << 23 : 1u << (16u + e)));
-}
-__device__ __forceinline__ int ckpt_q(float v, float inv) {
-  return max(-127, min(127, __float2int_rn(v * inv * 64.0f)));
-}
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Two fp32 values in one register pair: one instruction for both (the
 // activations are otherwise bound by instruction issue beside the memory).

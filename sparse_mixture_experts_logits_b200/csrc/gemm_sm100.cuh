@@ -57,6 +57,14 @@ enum GemmEpilogue : int {
   // the contraction taken out of the tensor cores every kSwChunk k-blocks.
   EPI_OUT_F32 = 12,
   EPI_OUT_BF16 = 13,        // out bf16 = acc (+ bias[g, n])
+  // Training with 8-bit checkpoints (tokens-on-N kernel only): the forward's
+  // first GEMM that also keeps its pre-activations, and the input-gradient
+  // GEMM that reads them back (EPI_BWD_*_DACT with h = the kept values, and
+  // out3 bf16 = w act(h)).
+  EPI_SWIGLU_KEEP = 14,
+  EPI_GELU_KEEP = 15,
+  EPI_KEPT_GELU_DACT = 16,
+  EPI_KEPT_SWIGLU_DACT = 17,
 };
 
 // Operand layouts of the tokens-on-N GEMM (gemm_swap_sm100.cuh): the forward

@@ -106,6 +106,8 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     switch (epi) {
       case EPI_STORE_F32: return launch_swap_epi<EPI_STORE_F32, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_KEPT_GELU_DACT: return launch_swap_epi<EPI_KEPT_GELU_DACT, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_KEPT_SWIGLU_DACT: return launch_swap_epi<EPI_KEPT_SWIGLU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_GELU_DACT: return launch_swap_epi<EPI_BWD_GELU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_BWD_SWIGLU_DACT: return launch_swap_epi<EPI_BWD_SWIGLU_DACT, kSwDgrad>(m, a, tiles_ub, s);
@@ -124,6 +126,8 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     case EPI_ACCUM_F32: return launch_swap_epi<EPI_ACCUM_F32>(m, a, tiles_ub, s);
     case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32>(m, a, tiles_ub, s);
     case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16>(m, a, tiles_ub, s);
+    case EPI_SWIGLU_KEEP: return launch_swap_epi<EPI_SWIGLU_KEEP>(m, a, tiles_ub, s);
+    case EPI_GELU_KEEP: return launch_swap_epi<EPI_GELU_KEEP>(m, a, tiles_ub, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -187,6 +191,9 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   a.tile_ctr = L.tile_ctr;
   a.accumulate = L.accumulate;
   a.clear_status = L.clear_status;
+  a.keep_q = L.keep_q;
+  a.keep_e = L.keep_e;
+  a.keep_blocks = (L.half_cols + kBlk - 1) / kBlk;
   if (is_wgrad(L.layout)) {
     const long long tiles_ub = static_cast<long long>(L.num_groups) * L.w_tiles * L.b_tiles;
     if (L.layout == kSwWgradRagged) {

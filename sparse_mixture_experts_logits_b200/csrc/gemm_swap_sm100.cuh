@@ -63,6 +63,7 @@
 // registers while the next chunk's MMAs fill the other accumulator.
 #pragma once
 
+#include "ckpt.cuh"
 #include "gemm_sm100.cuh"
 
 namespace moe {
@@ -184,6 +185,11 @@ struct SwapArgs {
   // (dynamic schedule); otherwise they take fixed rounds (swap_tile_at).
   int* tile_ctr;
   int accumulate;  // kSwWgradRagged: add onto the output
+  // EPI_*_KEEP write, EPI_KEPT_* read: q [rows][halves][half_cols] and its
+  // exponents [rows][halves][keep_blocks] (halves: 2 for SwiGLU, else 1)
+  int8_t* keep_q;
+  uint8_t* keep_e;
+  int keep_blocks;
   int clear_status;  // the first CTA clears *status at its start (nothing did before the launch)
 };
 
@@ -305,6 +311,39 @@ __device__ __forceinline__ float warp_transpose_sum(float (&v)[32], int lane) {
   return v[0];
 }
 
+// Keeps 32 rows (r[i]: row `row` + i of this lane's column `col`; the warp's
+// lanes are 32 consecutive columns, i.e. one block) of half `half` in 8 bits.
+// Four rows at a time: the block's exponent is a warp-wide maximum, and the
+// four lanes of a quad transpose their 4 x 4 bytes, so that lane j stores row
+// j's four columns as one word.  half_cols is a multiple of 16.
+__device__ __forceinline__ void keep_rows32(const SwapArgs& a, const float (&r)[32], size_t row, int nv, int col,
+                                            bool col_ok, int halves, int half, int lane) {
+  const int j = lane & 3;
+  int8_t* qp = a.keep_q + ((row + j) * halves + half) * a.half_cols + (col & ~3);
+  uint8_t* ep = a.keep_e + ((row + lane) * halves + half) * a.keep_blocks + ((col - lane) >> 5);
+  const size_t q4 = static_cast<size_t>(4 * halves) * a.half_cols, e4 = static_cast<size_t>(4 * halves) * a.keep_blocks;
+  const bool any = col - lane < a.half_cols;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4, qp += q4, ep += e4) {
+    uint32_t b[4], mine = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float v = col_ok ? r[i + t] : 0.f;
+      const uint32_t e = __reduce_max_sync(0xffffffffu, abs_bits(v)) >> 23;
+      const float u = fminf(fmaxf(v * ckpt_inv_scale(e), -127.0f / 64.0f), 127.0f / 64.0f);
+      b[t] = e == 255u ? 0u : __float_as_uint(fmaf(u, 64.0f, 12582912.0f));
+      if (lane == t) mine = e;
+    }
+    const uint32_t p = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    const uint32_t p1 = __shfl_xor_sync(0xffffffffu, p, 1);
+    const uint32_t x = __byte_perm(p, p1, (j & 1) ? 0x3715 : 0x6240);
+    const uint32_t x2 = __shfl_xor_sync(0xffffffffu, x, 2);
+    const uint32_t word = __byte_perm(x, x2, (j & 2) ? 0x3276 : 0x5410);
+    if (col_ok && i + j < nv) *reinterpret_cast<uint32_t*>(qp) = word;
+    if (any && lane < 4 && i + lane < nv) *ep = static_cast<uint8_t>(mine);
+  }
+}
+
 template <int EPI, int LAYOUT>
 __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
     moe_gemm_swap_kernel(const __grid_constant__ SwapMaps maps, const SwapArgs args) {
@@ -313,7 +352,8 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
   constexpr int S = LAYOUT == kSwWgrad ? kSwWgStages : LAYOUT == kSwWgradRagged ? kSwRgStages : kSwStages;
   constexpr int KB = swap_kb<LAYOUT>();
   constexpr int kStage = swap_stage_bytes<LAYOUT>();
-  constexpr bool kSwiglu = EPI == EPI_SWIGLU || EPI == EPI_BWD_SWIGLU_SAVE;
+  constexpr bool kSwiglu = EPI == EPI_SWIGLU || EPI == EPI_BWD_SWIGLU_SAVE || EPI == EPI_SWIGLU_KEEP;
+  constexpr bool kKeptDact = EPI == EPI_KEPT_GELU_DACT || EPI == EPI_KEPT_SWIGLU_DACT;
   constexpr bool kAMn = LAYOUT != kSwFwd;
   constexpr bool kBMn = kWgrad;
   static_assert(!(kSwiglu && LAYOUT != kSwFwd), "the gate/up pairing reads K-major weight rows");
@@ -681,7 +721,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const bool col_ok = col < args.out_cols;
       float bias = 0.f;
       if constexpr (EPI == EPI_GELU_BIAS || EPI == EPI_SCALE_BIAS || EPI == EPI_BIAS_ADD ||
-                    EPI == EPI_BWD_GELU_SAVE || EPI == EPI_OUT_BF16 || (EPI == EPI_OUT_F32 && !kWgrad)) {
+                    EPI == EPI_BWD_GELU_SAVE || EPI == EPI_GELU_KEEP || EPI == EPI_OUT_BF16 || (EPI == EPI_OUT_F32 && !kWgrad)) {
         if (args.bias != nullptr && col_ok)
           bias = __bfloat162float(args.bias[static_cast<size_t>(t.g) * args.out_cols + col]);
       }
@@ -692,8 +732,9 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256u;
       constexpr bool kScaled = EPI == EPI_SCALE_BIAS || EPI == EPI_BWD_GELU_SAVE ||
                                EPI == EPI_BWD_SWIGLU_SAVE || EPI == EPI_BWD_GELU_DACT ||
-                               EPI == EPI_BWD_SWIGLU_DACT;
-      constexpr bool kDact = EPI == EPI_BWD_GELU_DACT || EPI == EPI_BWD_SWIGLU_DACT;
+                               EPI == EPI_BWD_SWIGLU_DACT || kKeptDact;
+      constexpr bool kDact = EPI == EPI_BWD_GELU_DACT || EPI == EPI_BWD_SWIGLU_DACT || kKeptDact;
+      constexpr bool kDactSwiglu = EPI == EPI_BWD_SWIGLU_DACT || EPI == EPI_KEPT_SWIGLU_DACT;
       if constexpr (kChunked) {
         // The tile's sums in registers: this lane's column of the warp's up
         // to four pieces of 32 rows (weight gradients: 32 B columns).
@@ -872,7 +913,14 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           for (int i = 0; i < 32; ++i) {
             const bool live = col_ok && i < nvd;
             const size_t row = row0 + c + i;
-            if constexpr (kDact) {
+            if constexpr (kKeptDact) {
+              constexpr int kHalves = kDactSwiglu ? 2 : 1;
+              const int8_t* qr = args.keep_q + row * kHalves * args.half_cols + col;
+              const uint8_t* er = args.keep_e + row * kHalves * args.keep_blocks + (col >> 5);
+              hv[i] = live ? static_cast<float>(qr[0]) * ckpt_scale(er[0]) : 0.f;
+              if constexpr (kDactSwiglu)
+                uv[i] = live ? static_cast<float>(qr[args.half_cols]) * ckpt_scale(er[args.keep_blocks]) : 0.f;
+            } else if constexpr (kDact) {
               hv[i] = live ? args.aux[row * args.ld_aux + col] : 0.f;
               if constexpr (EPI == EPI_BWD_SWIGLU_DACT)
                 uv[i] = live ? args.aux[row * args.ld_aux + args.half_cols + col] : 0.f;
@@ -912,9 +960,15 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) xs[lane * kSwXPitch + i] = __uint_as_float(r[i]);
             mbar_arrive(smem_addr(&s_xfull[xpair]));
+            if constexpr (EPI == EPI_SWIGLU_KEEP) {
+              float u[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] = __uint_as_float(r[i]);
+              keep_rows32(args, u, row0 + c, nv, col, col_ok, 2, 1, lane);
+            }
           } else {
             if (!mbar_wait(smem_addr(&s_xfull[xpair]), xc & 1u, abort_flag, args.status)) { ok = false; break; }
-            if constexpr (EPI == EPI_SWIGLU) {
+            if constexpr (EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_KEEP) {
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = silu_fast(__uint_as_float(r[i])) * xs[lane * kSwXPitch + i];
@@ -923,6 +977,11 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (i < nv) swap_store<EPI>(args, row0 + c + i, col, v[i]);
+              }
+              if constexpr (EPI == EPI_SWIGLU_KEEP) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                keep_rows32(args, v, row0 + c, nv, col, col_ok, 2, 0, lane);
               }
             } else {  // EPI_BWD_SWIGLU_SAVE: g, u, a = SiLU(g) u, w a
               float u[32];
@@ -946,7 +1005,17 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
             }
           }
           ++xc;
-        } else if constexpr (EPI == EPI_BWD_GELU_DACT || EPI == EPI_BWD_SWIGLU_DACT) {
+        } else if constexpr (EPI == EPI_GELU_KEEP) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) + bias;
+          if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < nv) swap_store<EPI>(args, row0 + c + i, col, gelu_tanh_fast(v[i]));
+          }
+          keep_rows32(args, v, row0 + c, nv, col, col_ok, 1, 0, lane);
+        } else if constexpr (kDact) {
           // G = acc (the gradient reaching a, before the gate weight); dh out,
           // and per token the partial <G, a> over this warp's 32 columns
           float prod[32];
@@ -958,10 +1027,11 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
             prod[i] = 0.f;
             if (col_ok && i < nv) {
               const size_t row = row0 + c + i;
-              if constexpr (EPI == EPI_BWD_GELU_DACT) {
+              if constexpr (!kDactSwiglu) {
                 float a, da_dh;
                 gelu_tanh_and_grad_fast(hv[i], a, da_dh);
                 dh[row * args.ldo + col] = __float2bfloat16_rn(w * G * da_dh);
+                if constexpr (kKeptDact) args.out3[row * args.ldo2 + col] = __float2bfloat16_rn(w * a);
                 prod[i] = G * a;
               } else {
                 const float g = hv[i], u = uv[i];
@@ -970,6 +1040,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
                 const float da = w * G;
                 dh[row * args.ldo + col] = __float2bfloat16_rn(da * u * sg * fmaf(g, 1.0f - sg, 1.0f));
                 dh[row * args.ldo + args.half_cols + col] = __float2bfloat16_rn(da * si);
+                if constexpr (kKeptDact) args.out3[row * args.ldo2 + col] = __float2bfloat16_rn(w * si * u);
                 prod[i] = G * si * u;
               }
             }

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restr
                                                             uint4* __restrict__ x_tail, uint4* __restrict__ dy_tail,
                                                             uint4* __restrict__ out, float* __restrict__ db,
                                                             int* status) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
+  if (status != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
   const int g = blockIdx.y;
   if (blockIdx.z == 2) {
     __shared__ float2 part[8][32];
@@ -72,7 +72,7 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
   S.num_groups = L.G;
   S.offsets = L.offsets;
   S.rows = L.rows;
-  S.status = reinterpret_cast<int*>(base);
+  S.status = L.status != nullptr ? L.status : reinterpret_cast<int*>(base);
   S.w_tile_step = 256; S.w_hi_offset = 64; S.w_cta_step = 128;
   S.cols_per_tile = 256;
   S.out = L.out;
@@ -87,7 +87,7 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     wgrad_prepare_kernel<<<dim3(share, L.G, sums ? 3 : 2), 256, 0, s>>>(
         static_cast<const uint4*>(L.x), static_cast<const uint4*>(L.dy), L.offsets, L.rows, vk, vn, units,
         L.accumulate, reinterpret_cast<uint4*>(x_tail), reinterpret_cast<uint4*>(dy_tail), static_cast<uint4*>(L.out),
-        L.db, reinterpret_cast<int*>(base));
+        L.db, L.status != nullptr ? nullptr : reinterpret_cast<int*>(base));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (L.db != nullptr && !sums) {

@@ -105,6 +105,9 @@ struct SwapLaunch {
   const void* W_tail; const void* X_tail;
   int accumulate;
   int clear_status;          // clear *status in the launch itself
+  // EPI_*_KEEP, EPI_KEPT_*: the 8-bit checkpoint of the pre-activations
+  // (half_cols: the width of one half)
+  int8_t* keep_q; uint8_t* keep_e;
 };
 cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s);
 
@@ -127,6 +130,9 @@ struct GroupedLaunch {
   // grouped_colsum_shares(...) > 1, that many [G, N] of partial sums
   float* db;
   float* part;
+  // Tensor-core path: the status word that waits report to (null: the first
+  // word of the call's workspace, which the call clears).
+  int* status;
 };
 cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_t s);
 // grouped_tc.cu: the same products of bf16 operands on the tensor cores (N and

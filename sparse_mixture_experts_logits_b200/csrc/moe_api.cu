@@ -181,6 +181,34 @@ FwdWs forward_layout(const moe_layer_desc_t* d) {
   return L;
 }
 
+// A layer's checkpoint (moe_checkpoint_size): the routing that the forward
+// chose and every pre-activation in 8 bits, routed rows in dispatch order.
+struct CkptLayout { size_t idx, tw, logits, q, e, sq, se, total; };
+inline size_t ckpt_blocks(int cols) { return (static_cast<size_t>(cols) + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK; }
+CkptLayout ckpt_layout(const moe_layer_desc_t* d) {
+  Carve c;
+  CkptLayout L;
+  const size_t pairs = static_cast<size_t>(d->T) * d->k, T = d->T;
+  const size_t halves = d->act == MOE_ACT_SWIGLU ? 2 : 1;
+  L.idx = c.take(pairs * 4);
+  L.tw = c.take(pairs * 4);
+  L.logits = c.take(static_cast<size_t>(route_layout_splits(d->T, d->D, d->dtype)) * T * d->M * 4);
+  L.q = c.take(pairs * halves * d->I);
+  L.e = c.take(pairs * halves * ckpt_blocks(d->I));
+  L.sq = c.take(d->I_sh > 0 ? T * 2 * d->I_sh : 0);
+  L.se = c.take(d->I_sh > 0 ? T * 2 * ckpt_blocks(d->I_sh) : 0);
+  L.total = c.off;
+  return L;
+}
+
+// What a forward that keeps its pre-activations writes beside its results.
+// h: fp32 layers only, room for the widest pre-activations.
+struct Keep {
+  int8_t* q; uint8_t* e;
+  int8_t* sq; uint8_t* se;
+  float* h;
+};
+
 // ------------------------------------------------------------ the stages
 // Records caller-provided CUDA events at stage boundaries (profiled forward).
 // NVTX range around a host-side stage (shows the stages on a profiler's
@@ -239,7 +267,7 @@ moe_status_t run_experts(const moe_layer_desc_t* d, const moe_weights_t* w, cons
                          const int32_t* offsets, const int32_t* row_token, const float* row_w,
                          void* out_perm, void* x_perm, void* h, int* status, cudaStream_t s,
                          const Marks& mk = Marks(), const int32_t* slot_of = nullptr,
-                         int* tile_ctrs = nullptr) {
+                         int* tile_ctrs = nullptr, const Keep* keep = nullptr) {
   const int pairs = d->T * d->k;
   const bool swiglu = d->act == MOE_ACT_SWIGLU;
   const int n1 = swiglu ? 2 * d->I : d->I;
@@ -248,7 +276,7 @@ moe_status_t run_experts(const moe_layer_desc_t* d, const moe_weights_t* w, cons
   // A handful of rows per expert (decode): tokens on M with single-CTA MMAs. The 128-row token
   // tile is mostly padding, but each CTA streams its own slice of the touched experts'
   // weights once (measured: GLM-4.5 decode expert GEMMs 0.837 -> 0.810 ms).
-  if (d->dtype == MOE_DTYPE_BF16 && few_rows(d)) {
+  if (d->dtype == MOE_DTYPE_BF16 && few_rows(d) && keep == nullptr) {
     MOE_CUDA(launch_gather_rows(x, row_token, offsets + d->M, x_perm, pairs, d->T, d->D, 2, status, s));
     MOE_TRY(mk.at(3));
     GemmLaunch g1{};
@@ -313,6 +341,11 @@ moe_status_t run_experts(const moe_layer_desc_t* d, const moe_weights_t* w, cons
       g1.bias = b1;
     }
     g1.w_tiles = (d->I + g1.cols_per_tile - 1) / g1.cols_per_tile;
+    if (keep != nullptr) {
+      g1.epi = swiglu ? EPI_SWIGLU_KEEP : EPI_GELU_KEEP;
+      g1.keep_q = keep->q; g1.keep_e = keep->e;
+      g1.half_cols = d->I;
+    }
     g1.out_cols = d->I; g1.ldo = d->I; g1.out = h;
     g1.status = status;
     g1.tile_ctr = tile_ctrs;
@@ -343,7 +376,15 @@ moe_status_t run_experts(const moe_layer_desc_t* d, const moe_weights_t* w, cons
     g1.b_rows_per_group = n1; g1.swiglu_hi = swiglu ? d->I : 0;
     g1.out_cols = d->I; g1.ldo = d->I; g1.out = static_cast<float*>(h);
     g1.bias = static_cast<const float*>(b1);
+    if (keep != nullptr) {  // the pre-activations, then the activation that keeps them
+      g1.epi = EPI_BIAS_ADD;
+      g1.swiglu_hi = 0;
+      g1.out_cols = n1; g1.ldo = n1; g1.out = keep->h;
+    }
     MOE_CUDA(launch_simt_gemm(g1, s));
+    if (keep != nullptr)
+      MOE_CUDA(launch_act_save(MOE_DTYPE_F32, MOE_DTYPE_F32, swiglu, keep->h, offsets + d->M, pairs, d->I, h, keep->q,
+                               keep->e, s));
     MOE_TRY(mk.at(4));
     SimtLaunch g2{};
     g2.epi = EPI_SCALE_BIAS;
@@ -364,7 +405,7 @@ moe_status_t run_experts(const moe_layer_desc_t* d, const moe_weights_t* w, cons
 // combine), else in the layer's dtype.
 moe_status_t run_shared(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, void* out,
                         void* h_sh, bool out_f32, int* status, cudaStream_t s,
-                        const Marks& mk = Marks()) {
+                        const Marks& mk = Marks(), const Keep* keep = nullptr) {
   if (d->dtype == MOE_DTYPE_BF16) {
     SwapLaunch g1{};
     g1.epi = EPI_SWIGLU;
@@ -374,6 +415,11 @@ moe_status_t run_shared(const moe_layer_desc_t* d, const moe_weights_t* w, const
     g1.num_groups = 1; g1.offsets = nullptr; g1.rows = d->T;
     g1.w_rows_per_group = 2 * d->I_sh; g1.w_tile_step = 128; g1.w_hi_offset = d->I_sh; g1.w_cta_step = 64;
     g1.cols_per_tile = 128; g1.w_tiles = (d->I_sh + 127) / 128;
+    if (keep != nullptr) {
+      g1.epi = EPI_SWIGLU_KEEP;
+      g1.keep_q = keep->sq; g1.keep_e = keep->se;
+      g1.half_cols = d->I_sh;
+    }
     g1.out_cols = d->I_sh; g1.ldo = d->I_sh; g1.out = h_sh;
     g1.status = status;
     MOE_CUDA(launch_gemm_swap(g1, s));
@@ -397,7 +443,15 @@ moe_status_t run_shared(const moe_layer_desc_t* d, const moe_weights_t* w, const
     g1.num_groups = 1; g1.offsets = nullptr; g1.rows = d->T;
     g1.b_rows_per_group = 2 * d->I_sh; g1.swiglu_hi = d->I_sh;
     g1.out_cols = d->I_sh; g1.ldo = d->I_sh; g1.out = static_cast<float*>(h_sh);
+    if (keep != nullptr) {
+      g1.epi = EPI_STORE_F32;
+      g1.swiglu_hi = 0;
+      g1.out_cols = 2 * d->I_sh; g1.ldo = 2 * d->I_sh; g1.out = keep->h;
+    }
     MOE_CUDA(launch_simt_gemm(g1, s));
+    if (keep != nullptr)
+      MOE_CUDA(launch_act_save(MOE_DTYPE_F32, MOE_DTYPE_F32, true, keep->h, nullptr, d->T, d->I_sh, h_sh, keep->sq,
+                               keep->se, s));
     MOE_TRY(mk.at(6));
     SimtLaunch g2{};
     g2.epi = EPI_STORE_F32;
@@ -833,7 +887,7 @@ moe_status_t moe_workspace_layout(const moe_layer_desc_t* d, moe_ws_layout_t* ou
 
 static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x,
                                  const void* addend, void* y, void* ws, size_t ws_bytes, cudaStream_t s,
-                                 void* const* events) {
+                                 void* const* events, void* ckpt = nullptr, const Keep* keep = nullptr) {
   MOE_TRY(check_desc(d));
   MOE_TRY(check_weights(d, w, true, true));
   if (w->w_r == nullptr) return MOE_ERR_INVALID_ARG;
@@ -855,6 +909,13 @@ static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t*
   int32_t* row_token = at<int32_t*>(ws, L.pub.row_token);
   float* row_w = at<float*>(ws, L.pub.row_w);
   void* out_perm = at<void*>(ws, L.pub.out_perm);
+  float* logits = at<float*>(ws, L.logits);
+  if (keep != nullptr) {  // the routing goes to the checkpoint
+    const CkptLayout C = ckpt_layout(d);
+    idx = at<int32_t*>(ckpt, C.idx);
+    tw = at<float*>(ckpt, C.tw);
+    logits = at<float*>(ckpt, C.logits);
+  }
   Range whole("moe_forward");
   // the status flag and, in the same 256-byte slot of the workspace, the
   // tile counters of the two routed expert GEMMs (ints 2 and 3), which
@@ -870,7 +931,7 @@ static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t*
   void* y_sh = d->I_sh > 0 ? at<void*>(ws, L.y_sh) : nullptr;
   SideFork shared_fork;
   bool shared_done = false;
-  if (d->I_sh > 0 && d->dtype == MOE_DTYPE_BF16 && few_rows(d)) {
+  if (d->I_sh > 0 && d->dtype == MOE_DTYPE_BF16 && few_rows(d) && keep == nullptr) {
     if (SideStream* side = side_stream(s)) {
       Range r("moe.shared_expert");
       MOE_TRY(shared_fork.fork(side, s));
@@ -882,8 +943,8 @@ static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t*
   {
     Range r("moe.route");
     MOE_TRY(run_route(x, w->w_r, w->e_bias, d->T, d->D, d->M, d->k, d->dtype, d->gate, d->norm_topk_prob,
-                      d->routed_scaling_factor, d->eps, d->n_group, d->topk_group, idx, tw,
-                      at<float*>(ws, L.logits), at<void*>(ws, L.wrT), status, s));
+                      d->routed_scaling_factor, d->eps, d->n_group, d->topk_group, idx, tw, logits,
+                      at<void*>(ws, L.wrT), status, s));
   }
   MOE_TRY(mk.at(1));
   {
@@ -899,7 +960,7 @@ static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t*
   {
     Range r("moe.experts");
     MOE_TRY(run_experts(d, w, x, offsets, row_token, row_w, out_perm, at<void*>(ws, L.x_perm),
-                        at<void*>(ws, L.h), status, s, mk, by_token ? slot_of : nullptr, tile_ctrs));
+                        at<void*>(ws, L.h), status, s, mk, by_token ? slot_of : nullptr, tile_ctrs, keep));
   }
   if (shared_done) {
     MOE_TRY(shared_fork.join());
@@ -907,7 +968,7 @@ static moe_status_t forward_impl(const moe_layer_desc_t* d, const moe_weights_t*
     MOE_TRY(mk.at(7));
   } else if (d->I_sh > 0) {
     Range r("moe.shared_expert");
-    MOE_TRY(run_shared(d, w, x, y_sh, at<void*>(ws, L.h_sh), true, status, s, mk));
+    MOE_TRY(run_shared(d, w, x, y_sh, at<void*>(ws, L.h_sh), true, status, s, mk, keep));
   } else {
     MOE_TRY(mk.at(6));
     MOE_TRY(mk.at(7));
@@ -1130,6 +1191,251 @@ SwapLaunch bwd_swap(int epi, int layout, const void* A, long long a_rows, const 
   return L;
 }
 
+// The shared expert's backward: its weight gradients, and its dx into dxs
+// (fp32).  The pre-activations are recomputed into hsb (fp32), or read from
+// the checkpoint (sq, se); asb gets a = act(h), dhsb dL/dh.
+moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
+                                const moe_grads_t* g, void* hsb, int8_t* sq, uint8_t* se, void* asb, void* dhsb,
+                                float* dxs, int* status, cudaStream_t s) {
+  const int T = d->T, D = d->D, Is = d->I_sh;
+  const bool kept = sq != nullptr;
+  if (Is > 0) {
+    Range r("moe.shared_expert_backward");
+    if (!kept) {
+      SwapLaunch sa = bwd_swap(EPI_BWD_SWIGLU_SAVE, kSwFwd, w->sh_w1, 2ll * Is, x, T, D, 1, nullptr, nullptr, T, Is,
+                               hsb, 2 * Is, status);
+      sa.w_rows_per_group = 2 * Is;
+      sa.w_tiles = (Is + 127) / 128;
+      sa.w_tile_step = 128;
+      sa.w_hi_offset = Is;
+      sa.w_cta_step = 64;
+      sa.cols_per_tile = 128;
+      sa.half_cols = Is;
+      sa.out2 = asb;
+      sa.ldo2 = Is;
+      MOE_CUDA(launch_gemm_swap(sa, s));
+    }
+    SwapLaunch sb = bwd_swap(kept ? EPI_KEPT_SWIGLU_DACT : EPI_BWD_SWIGLU_DACT, kSwDgrad, w->sh_w2, D, dy, T, D, 1, nullptr, nullptr, T, Is, dhsb,
+                             2 * Is, status);
+    sb.k_rows_per_group = D;
+    sb.aux = hsb;
+    sb.ld_aux = 2 * Is;
+    sb.half_cols = Is;
+    sb.keep_q = sq;
+    sb.keep_e = se;
+    sb.out3 = asb;
+    sb.ldo2 = Is;
+    MOE_CUDA(launch_gemm_swap(sb, s));
+    SwapLaunch sc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->sh_w1, 2ll * Is, dhsb, T, 2 * Is, 1, nullptr, nullptr, T,
+                             D, dxs, D, status);
+    sc.k_rows_per_group = 2 * Is;
+    MOE_CUDA(launch_gemm_swap(sc, s));
+    SwapLaunch sd = bwd_swap(EPI_STORE_F32, kSwWgrad, asb, T, dy, T, 0, 1, nullptr, nullptr, T, Is, g->dsh_w2, Is,
+                             status);
+    sd.b_cols = D;
+    sd.b_tiles = (D + 255) / 256;
+    MOE_CUDA(launch_gemm_swap(sd, s));
+    SwapLaunch se = bwd_swap(EPI_STORE_F32, kSwWgrad, x, T, dhsb, T, 0, 1, nullptr, nullptr, T, D, g->dsh_w1, D,
+                             status);
+    se.b_cols = 2 * Is;
+    se.b_tiles = (2 * Is + 255) / 256;
+    MOE_CUDA(launch_gemm_swap(se, s));
+  }
+  return MOE_OK;
+}
+
+// The router's backward: dW_r, and its dx added onto (or, without a shared
+// expert, written to) dxs.  dlb: bf16 dlogits when the two products run on the
+// tensor cores, else null and rpart holds the chunk sums of dW_r.
+moe_status_t router_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const float* logits,
+                                const int32_t* idx, const float* dwp, float* dl, void* dlb, float* dxs, float* rpart,
+                                const moe_grads_t* g, int* status, cudaStream_t s) {
+  const int T = d->T, D = d->D, M = d->M, k = d->k, Is = d->I_sh;
+  {
+    Range r("moe.router_backward");
+    const bool tc = dlb != nullptr;
+    MOE_CUDA(launch_bwd_router(logits, idx, dwp, T, M, k, d->gate, d->norm_topk_prob, d->routed_scaling_factor,
+                               d->eps, dl, dlb, s));
+    if (tc) {
+      // dW_r [D, M] = x^T dlogits: the weight-gradient layout over one group of T rows,
+      // dlogits (bf16) on the A side so that its M columns are the output's contiguous ones
+      SwapLaunch gw = bwd_swap(EPI_STORE_F32, kSwWgrad, dlb, T, x, T, 0, 1, nullptr, nullptr, T, M, g->dw_r, M,
+                               status);
+      gw.b_cols = D;
+      gw.b_tiles = (D + 255) / 256;
+      gw.out_gstride = 1ll * D * M;
+      MOE_CUDA(launch_gemm_swap(gw, s));
+      // dx += dlogits W_r^T: the forward layout, W_r [D, M] as K-major weight rows (K = M),
+      // added onto the shared expert's dx when there is one
+      SwapLaunch gx = bwd_swap(Is > 0 ? EPI_ACCUM_F32 : EPI_STORE_F32, kSwFwd, w->w_r, D, dlb, T, M, 1, nullptr,
+                               nullptr, T, D, dxs, D, status);
+      MOE_CUDA(launch_gemm_swap(gx, s));
+    } else {
+      BwdGemmLaunch wr = bwd_gemm(x, 1, D, true, dl, 1, M, 0, false, g->dw_r, M, D, T, M);
+      wr.mode = 1;
+      wr.ksplit = router_ksplit(T);
+      wr.partial = rpart;
+      MOE_CUDA(launch_bwd_gemm(wr, s));
+      BwdGemmLaunch xr = bwd_gemm(dl, M, 1, false, w->w_r, M, 1, 0, true, dxs, D, T, M, D);
+      xr.accumulate = Is > 0 ? 1 : 0;  // onto the shared expert's dx
+      MOE_CUDA(launch_bwd_gemm(xr, s));
+    }
+  }
+  return MOE_OK;
+}
+
+// The workspace of moe_backward_saved: the dispatch order, recomputed from
+// the checkpoint's indices, and the rows' tensors in it.
+struct SavedWs {
+  size_t status, counts, offsets, slot_of, row_token, row_w, chunk_counts, chunk_base;
+  size_t xp, dyp, wa, dh, dxp, parts, dwp, dl, as, dhs, dxs, rpart, dlb, wgrad, colsum, total;
+  size_t hpre, act, dO, o, hs, das;  // fp32 layers
+};
+SavedWs saved_layout(const moe_layer_desc_t* d) {
+  SavedWs L{};
+  Carve c;
+  const size_t pairs = static_cast<size_t>(d->T) * d->k;
+  const size_t n1 = d->act == MOE_ACT_SWIGLU ? 2ull * d->I : static_cast<size_t>(d->I);
+  const size_t Ha = d->I, T = d->T, Is = d->I_sh, D = d->D, M = d->M;
+  const bool bf = d->dtype == MOE_DTYPE_BF16;
+  L.status = c.take(4);
+  L.counts = c.take(M * 4);
+  L.offsets = c.take((M + 1) * 4);
+  L.slot_of = c.take(pairs * 4);
+  L.row_token = c.take(pairs * 4);
+  L.row_w = c.take(pairs * 4);
+  const size_t nch = M * perm_num_chunks(static_cast<long long>(pairs));
+  L.chunk_counts = c.take(nch * 4);
+  L.chunk_base = c.take(nch * 4);
+  L.xp = c.take(pairs * D * esize(d->dtype));
+  L.dxp = c.take(pairs * D * 4);
+  L.dwp = c.take(pairs * 4);
+  L.dl = c.take(T * M * 4);
+  L.dxs = c.take(T * D * 4);
+  if (bf) {
+    L.dyp = c.take(pairs * D * 2);
+    L.wa = c.take(pairs * Ha * 2);
+    L.dh = c.take(pairs * n1 * 2);
+    L.parts = c.take(pairs * ((Ha + 31) / 32) * 4);
+    L.as = c.take(T * Is * 2);
+    L.dhs = c.take(T * 2 * Is * 2);
+    L.rpart = router_bwd_tc(d) ? 0 : c.take(static_cast<size_t>(router_ksplit(d->T)) * D * M * 4);
+    L.dlb = router_bwd_tc(d) ? c.take(T * M * 2) : 0;
+    L.wgrad = c.take(std::max(grouped_tc_workspace(kGroupedWgrad, d->M, d->D, d->I),
+                              grouped_tc_workspace(kGroupedWgrad, d->M, static_cast<int>(n1), d->D)));
+    const int shares = grouped_colsum_shares(d->M, static_cast<int>(pairs), d->I);
+    L.colsum = c.take(shares > 1 ? static_cast<size_t>(shares) * M * Ha * 4 : 0);
+  } else {
+    L.hpre = c.take(pairs * n1 * 4);
+    L.act = c.take(pairs * Ha * 4);
+    L.o = c.take(pairs * D * 4);
+    L.dO = c.take(pairs * D * 4);
+    L.wa = c.take(pairs * Ha * 4);
+    L.hs = c.take(T * 2 * Is * 4);
+    L.as = c.take(T * Is * 4);
+    L.das = c.take(T * Is * 4);
+  }
+  L.total = c.off;
+  return L;
+}
+
+// The backward of a bf16 layer from its checkpoint.  As backward_tc_impl, but
+// the routing and the pre-activations are read instead of recomputed (one
+// product of five less, and no fp32 pre-activations in memory), and the rows
+// stay in the plain dispatch order: the ragged weight gradients need no padded
+// copies.  Per expert segment, with h' the kept values:
+//   G = dy W2;  dh = w G act'(h');  wa = w act(h');  parts = <G, act(h')>   (one fused epilogue)
+//   dx_rows = dh W1;  dW2 = dy^T wa;  dW1 = dh^T x
+moe_status_t saved_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
+                               void* ckpt, const moe_grads_t* g, void* ws, cudaStream_t s) {
+  const bool swiglu = d->act == MOE_ACT_SWIGLU;
+  const bool biases = !swiglu && d->has_bias;
+  const SavedWs L = saved_layout(d);
+  const CkptLayout C = ckpt_layout(d);
+  const int T = d->T, D = d->D, M = d->M, k = d->k, Ha = d->I;
+  const int n1 = swiglu ? 2 * d->I : d->I;
+  const int pairs = T * k;
+  const int nparts = (Ha + 31) / 32;
+  int* status = at<int*>(ws, L.status);
+  const int32_t* idx = at<int32_t*>(ckpt, C.idx);
+  const float* tw = at<float*>(ckpt, C.tw);
+  const float* logits = at<float*>(ckpt, C.logits);
+  int32_t* counts = at<int32_t*>(ws, L.counts);
+  int32_t* offsets = at<int32_t*>(ws, L.offsets);
+  int32_t* slot_of = at<int32_t*>(ws, L.slot_of);
+  int32_t* row_token = at<int32_t*>(ws, L.row_token);
+  float* row_w = at<float*>(ws, L.row_w);
+  void* xp = at<void*>(ws, L.xp);
+  void* dyp = at<void*>(ws, L.dyp);
+  void* wa = at<void*>(ws, L.wa);
+  void* dh = at<void*>(ws, L.dh);
+  float* dxp = at<float*>(ws, L.dxp);
+  float* parts = at<float*>(ws, L.parts);
+  float* dwp = at<float*>(ws, L.dwp);
+  float* dxs = at<float*>(ws, L.dxs);
+  Range whole("moe_backward_saved");
+  MOE_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
+  {
+    Range r("moe.dispatch");
+    MOE_CUDA(launch_permute(idx, tw, T, k, M, counts, offsets, slot_of, row_token, row_w,
+                            at<int32_t*>(ws, L.chunk_counts), at<int32_t*>(ws, L.chunk_base), status, s));
+    // as in the forward: large x and dy are read once and written k times
+    if (static_cast<double>(T) * D * 2 > 64.0 * 1024 * 1024) {
+      MOE_CUDA(launch_scatter_rows(x, slot_of, xp, T, k, D, status, s));
+      MOE_CUDA(launch_scatter_rows(dy, slot_of, dyp, T, k, D, status, s));
+    } else {
+      MOE_CUDA(launch_gather_rows(x, row_token, offsets + M, xp, pairs, T, D, 2, status, s));
+      MOE_CUDA(launch_gather_rows(dy, row_token, offsets + M, dyp, pairs, T, D, 2, status, s));
+    }
+  }
+  {
+    Range r("moe.experts_backward");
+    SwapLaunch gb = bwd_swap(swiglu ? EPI_KEPT_SWIGLU_DACT : EPI_KEPT_GELU_DACT, kSwDgrad, w->w2, 1ll * M * D, dyp,
+                             pairs, D, M, offsets, nullptr, pairs, Ha, dh, n1, status);
+    gb.k_rows_per_group = D;
+    gb.keep_q = at<int8_t*>(ckpt, C.q);
+    gb.keep_e = at<uint8_t*>(ckpt, C.e);
+    gb.half_cols = Ha;
+    gb.row_scale = row_w;
+    gb.parts = parts;
+    gb.ld_parts = nparts;
+    gb.out3 = wa;
+    gb.ldo2 = Ha;
+    MOE_CUDA(launch_gemm_swap(gb, s));
+    SwapLaunch gc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->w1, 1ll * M * n1, dh, pairs, n1, M, offsets, nullptr, pairs, D,
+                             dxp, D, status);
+    gc.k_rows_per_group = n1;
+    MOE_CUDA(launch_gemm_swap(gc, s));
+    GroupedLaunch gd{};
+    gd.dir = kGroupedWgrad;
+    gd.dtype = MOE_DTYPE_BF16; gd.out_dtype = MOE_DTYPE_F32;
+    gd.G = M; gd.rows = pairs;
+    gd.offsets = offsets;
+    gd.status = status;
+    gd.N = D; gd.K = Ha;
+    gd.x = wa; gd.dy = dyp; gd.out = g->dw2;
+    MOE_CUDA(launch_grouped_tc(gd, at<void*>(ws, L.wgrad), s));
+    gd.N = n1; gd.K = D;
+    gd.x = xp; gd.dy = dh; gd.out = g->dw1;
+    gd.db = biases ? g->db1 : nullptr;
+    gd.part = at<float*>(ws, L.colsum);
+    MOE_CUDA(launch_grouped_tc(gd, at<void*>(ws, L.wgrad), s));
+    MOE_CUDA(launch_dw_finish(parts, nparts, slot_of, idx, dy, biases ? w->b2 : nullptr, D, M, T, k, dwp, s));
+    if (biases) MOE_CUDA(launch_colsum_bf16(dyp, D, row_w, offsets, M, pairs, D, g->db2, s));
+  }
+  if (d->I_sh > 0)
+    MOE_TRY(shared_backward_tc(d, w, x, dy, g, nullptr, at<int8_t*>(ckpt, C.sq), at<uint8_t*>(ckpt, C.se),
+                               at<void*>(ws, L.as), at<void*>(ws, L.dhs), dxs, status, s));
+  MOE_TRY(router_backward_tc(d, w, x, logits, idx, dwp, at<float*>(ws, L.dl),
+                             router_bwd_tc(d) ? at<void*>(ws, L.dlb) : nullptr, dxs,
+                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), g, status, s));
+  {
+    Range r("moe.combine_backward");
+    MOE_CUDA(launch_combine(d->dtype, dxp, slot_of, dxs, true, nullptr, g->dx, T, D, k, s));
+  }
+  return MOE_OK;
+}
+
 // The backward of a bf16 layer on the tensor cores.  Per expert segment
 // (rows r of the padded dispatch order, token t(r), gate weight w_r):
 //   recompute  h = x W1^T (+ b1) (fp32), a = act(h), aw = w a   (save epilogue)
@@ -1255,76 +1561,10 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
       MOE_CUDA(launch_colsum_bf16(dhb, n1, nullptr, offp, M, P, Ha, g->db1, s));
     }
   }
-  if (Is > 0) {
-    Range r("moe.shared_expert_backward");
-    void* hsb = at<void*>(ws, L.hsb);
-    void* asb = at<void*>(ws, L.asb);
-    void* dhsb = at<void*>(ws, L.dhsb);
-    SwapLaunch sa = bwd_swap(EPI_BWD_SWIGLU_SAVE, kSwFwd, w->sh_w1, 2ll * Is, x, T, D, 1, nullptr, nullptr, T, Is,
-                             hsb, 2 * Is, status);
-    sa.w_rows_per_group = 2 * Is;
-    sa.w_tiles = (Is + 127) / 128;
-    sa.w_tile_step = 128;
-    sa.w_hi_offset = Is;
-    sa.w_cta_step = 64;
-    sa.cols_per_tile = 128;
-    sa.half_cols = Is;
-    sa.out2 = asb;
-    sa.ldo2 = Is;
-    MOE_CUDA(launch_gemm_swap(sa, s));
-    SwapLaunch sb = bwd_swap(EPI_BWD_SWIGLU_DACT, kSwDgrad, w->sh_w2, D, dy, T, D, 1, nullptr, nullptr, T, Is, dhsb,
-                             2 * Is, status);
-    sb.k_rows_per_group = D;
-    sb.aux = hsb;
-    sb.ld_aux = 2 * Is;
-    sb.half_cols = Is;
-    MOE_CUDA(launch_gemm_swap(sb, s));
-    SwapLaunch sc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->sh_w1, 2ll * Is, dhsb, T, 2 * Is, 1, nullptr, nullptr, T,
-                             D, dxs, D, status);
-    sc.k_rows_per_group = 2 * Is;
-    MOE_CUDA(launch_gemm_swap(sc, s));
-    SwapLaunch sd = bwd_swap(EPI_STORE_F32, kSwWgrad, asb, T, dy, T, 0, 1, nullptr, nullptr, T, Is, g->dsh_w2, Is,
-                             status);
-    sd.b_cols = D;
-    sd.b_tiles = (D + 255) / 256;
-    MOE_CUDA(launch_gemm_swap(sd, s));
-    SwapLaunch se = bwd_swap(EPI_STORE_F32, kSwWgrad, x, T, dhsb, T, 0, 1, nullptr, nullptr, T, D, g->dsh_w1, D,
-                             status);
-    se.b_cols = 2 * Is;
-    se.b_tiles = (2 * Is + 255) / 256;
-    MOE_CUDA(launch_gemm_swap(se, s));
-  }
-  {
-    Range r("moe.router_backward");
-    const bool tc = router_bwd_tc(d);
-    void* dlb = tc ? at<void*>(ws, L.dlb) : nullptr;
-    MOE_CUDA(launch_bwd_router(logits, idx, dwp, T, M, k, d->gate, d->norm_topk_prob, d->routed_scaling_factor,
-                               d->eps, dl, dlb, s));
-    if (tc) {
-      // dW_r [D, M] = x^T dlogits: the weight-gradient layout over one group of T rows,
-      // dlogits (bf16) on the A side so that its M columns are the output's contiguous ones
-      SwapLaunch gw = bwd_swap(EPI_STORE_F32, kSwWgrad, dlb, T, x, T, 0, 1, nullptr, nullptr, T, M, g->dw_r, M,
-                               status);
-      gw.b_cols = D;
-      gw.b_tiles = (D + 255) / 256;
-      gw.out_gstride = 1ll * D * M;
-      MOE_CUDA(launch_gemm_swap(gw, s));
-      // dx += dlogits W_r^T: the forward layout, W_r [D, M] as K-major weight rows (K = M),
-      // added onto the shared expert's dx when there is one
-      SwapLaunch gx = bwd_swap(Is > 0 ? EPI_ACCUM_F32 : EPI_STORE_F32, kSwFwd, w->w_r, D, dlb, T, M, 1, nullptr,
-                               nullptr, T, D, dxs, D, status);
-      MOE_CUDA(launch_gemm_swap(gx, s));
-    } else {
-      BwdGemmLaunch wr = bwd_gemm(x, 1, D, true, dl, 1, M, 0, false, g->dw_r, M, D, T, M);
-      wr.mode = 1;
-      wr.ksplit = router_ksplit(T);
-      wr.partial = at<float*>(ws, L.rpart);
-      MOE_CUDA(launch_bwd_gemm(wr, s));
-      BwdGemmLaunch xr = bwd_gemm(dl, M, 1, false, w->w_r, M, 1, 0, true, dxs, D, T, M, D);
-      xr.accumulate = Is > 0 ? 1 : 0;  // onto the shared expert's dx
-      MOE_CUDA(launch_bwd_gemm(xr, s));
-    }
-  }
+  MOE_TRY(shared_backward_tc(d, w, x, dy, g, at<void*>(ws, L.hsb), nullptr, nullptr, at<void*>(ws, L.asb),
+                             at<void*>(ws, L.dhsb), dxs, status, s));
+  MOE_TRY(router_backward_tc(d, w, x, logits, idx, dwp, dl, router_bwd_tc(d) ? at<void*>(ws, L.dlb) : nullptr, dxs,
+                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), g, status, s));
   {
     Range r("moe.combine_backward");
     MOE_CUDA(launch_combine(d->dtype, dxpp, slotp, dxs, true, nullptr, g->dx, T, D, k, s));
@@ -1335,43 +1575,46 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
   return MOE_OK;
 }
 
-moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
-                           const moe_grads_t* g, void* ws, size_t ws_bytes, cudaStream_t s) {
-  MOE_TRY(check_desc(d));
-  MOE_TRY(check_weights(d, w, true, true));
-  if (w->w_r == nullptr || g == nullptr) return MOE_ERR_INVALID_ARG;
+// Where the fp32 backward keeps its tensors: idx, tw and logits in the
+// workspace, or (from a checkpoint) in the checkpoint; all else in the
+// workspace.
+struct F32Ws {
+  size_t status, idx, tw, logits, counts, offsets, slot_of, row_token, row_w, chunk_counts, chunk_base, o, xp, hpre,
+      act, dO, da, dxp, dwp, dl, dxs, hs, as, das;
+};
+F32Ws plain_f32_ws(const BwdWs& L) {
+  return {L.f.pub.status,    L.f.pub.topk_idx,  L.f.pub.topk_w, L.f.logits,       L.f.pub.counts,  L.f.pub.offsets,
+          L.f.pub.slot_of,   L.f.pub.row_token, L.f.pub.row_w,  L.f.chunk_counts, L.f.chunk_base,  L.f.pub.out_perm,
+          L.xp,              L.hpre,            L.act,          L.dO,             L.da,            L.dxp,
+          L.dwp,             L.dl,              L.dxs,          L.hs,             L.as,            L.das};
+}
+F32Ws saved_f32_ws(const moe_layer_desc_t* d) {
+  const SavedWs L = saved_layout(d);
+  const CkptLayout C = ckpt_layout(d);
+  return {L.status, C.idx, C.tw, C.logits, L.counts, L.offsets, L.slot_of, L.row_token, L.row_w, L.chunk_counts,
+          L.chunk_base, L.o, L.xp, L.hpre, L.act, L.dO, L.wa, L.dxp, L.dwp, L.dl, L.dxs, L.hs, L.as, L.das};
+}
+
+// The backward of an fp32 layer, on the CUDA cores.
+moe_status_t backward_f32(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
+                          const moe_grads_t* g, void* ws, const F32Ws& L, void* ckpt, cudaStream_t s) {
+  const CkptLayout C = ckpt_layout(d);
+  const bool bf = false;
   const bool swiglu = d->act == MOE_ACT_SWIGLU;
   const bool biases = !swiglu && d->has_bias;
-  if (!g->dw_r || !g->dw1 || !g->dw2) return MOE_ERR_INVALID_ARG;
-  if (biases && (!g->db1 || !g->db2)) return MOE_ERR_INVALID_ARG;
-  if (d->I_sh > 0 && (!g->dsh_w1 || !g->dsh_w2)) return MOE_ERR_INVALID_ARG;
-  if (d->T == 0) {
-    MOE_TRY(check_device());
-    return zero_param_grads(d, g, s);
-  }
-  if (!x || !dy || !g->dx || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
-  if (d->dtype == MOE_DTYPE_BF16) {
-    if (!al16(x) || !al16(dy) || !al16(w->w_r) || !al16(g->dw1) || !al16(g->dw2)) return MOE_ERR_INVALID_ARG;
-    if (d->I_sh > 0 && (!al16(g->dsh_w1) || !al16(g->dsh_w2))) return MOE_ERR_INVALID_ARG;
-  }
-  const BwdWs L = backward_layout(d);
-  if (ws_bytes < L.total) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_device());
-  if (d->dtype == MOE_DTYPE_BF16) return backward_tc_impl(d, w, x, dy, g, ws, s);
-  const bool bf = d->dtype == MOE_DTYPE_BF16;
   const int T = d->T, D = d->D, M = d->M, k = d->k, Ha = d->I, Is = d->I_sh;
   const int n1 = swiglu ? 2 * d->I : d->I;
   const long long pairs = static_cast<long long>(T) * k;
-  int* status = at<int*>(ws, L.f.pub.status);
-  int32_t* idx = at<int32_t*>(ws, L.f.pub.topk_idx);
-  float* tw = at<float*>(ws, L.f.pub.topk_w);
-  int32_t* counts = at<int32_t*>(ws, L.f.pub.counts);
-  int32_t* offsets = at<int32_t*>(ws, L.f.pub.offsets);
-  int32_t* slot_of = at<int32_t*>(ws, L.f.pub.slot_of);
-  int32_t* row_token = at<int32_t*>(ws, L.f.pub.row_token);
-  float* row_w = at<float*>(ws, L.f.pub.row_w);
-  float* logits = at<float*>(ws, L.f.logits);
-  float* o = at<float*>(ws, L.f.pub.out_perm);
+  int* status = at<int*>(ws, L.status);
+  int32_t* idx = at<int32_t*>(ckpt != nullptr ? ckpt : ws, L.idx);
+  float* tw = at<float*>(ckpt != nullptr ? ckpt : ws, L.tw);
+  float* logits = at<float*>(ckpt != nullptr ? ckpt : ws, L.logits);
+  int32_t* counts = at<int32_t*>(ws, L.counts);
+  int32_t* offsets = at<int32_t*>(ws, L.offsets);
+  int32_t* slot_of = at<int32_t*>(ws, L.slot_of);
+  int32_t* row_token = at<int32_t*>(ws, L.row_token);
+  float* row_w = at<float*>(ws, L.row_w);
+  float* o = at<float*>(ws, L.o);
   void* xp = at<void*>(ws, L.xp);
   float* hpre = at<float*>(ws, L.hpre);
   float* act = at<float*>(ws, L.act);
@@ -1384,16 +1627,16 @@ moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, co
   const int32_t* n_rows = offsets + M;  // pairs dispatched
   Range whole("moe_backward");
   MOE_CUDA(cudaMemsetAsync(status, 0, sizeof(int), s));
-  {
+  if (ckpt == nullptr) {
     Range r("moe.route");
     MOE_TRY(run_route(x, w->w_r, w->e_bias, T, D, M, k, d->dtype, d->gate, d->norm_topk_prob,
                       d->routed_scaling_factor, d->eps, d->n_group, d->topk_group, idx, tw, logits,
-                      at<void*>(ws, L.f.wrT), status, s));
+                      nullptr, status, s));
   }
   {
     Range r("moe.dispatch");
     MOE_CUDA(launch_permute(idx, tw, T, k, M, counts, offsets, slot_of, row_token, row_w,
-                            at<int32_t*>(ws, L.f.chunk_counts), at<int32_t*>(ws, L.f.chunk_base), status, s));
+                            at<int32_t*>(ws, L.chunk_counts), at<int32_t*>(ws, L.chunk_base), status, s));
     MOE_CUDA(launch_gather_rows(x, row_token, n_rows, xp, static_cast<int>(pairs), T, D,
                                 static_cast<int>(esize(d->dtype)), status, s));
   }
@@ -1403,7 +1646,13 @@ moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, co
     BwdGemmLaunch g1 = bwd_gemm(xp, D, 1, bf, w->w1, D, 1, 1ll * n1 * D, bf, hpre, n1, pairs, D, n1);
     g1.offsets = offsets; g1.G = M;
     g1.bias = biases ? w->b1 : nullptr; g1.bias_gstride = Ha;
-    MOE_CUDA(launch_bwd_gemm(g1, s));
+    if (ckpt == nullptr) {
+      MOE_CUDA(launch_bwd_gemm(g1, s));
+    } else {  // the kept ones (a SwiGLU row is two rows of I columns)
+      const int rows = static_cast<int>(pairs) * (n1 / Ha);
+      MOE_CUDA(launch_ckpt_dequantize(MOE_DTYPE_F32, at<int8_t*>(ckpt, C.q), at<uint8_t*>(ckpt, C.e), nullptr, nullptr,
+                                      rows, rows, Ha, hpre, status, s));
+    }
     MOE_CUDA(launch_bwd_act(hpre, act, n_rows, pairs, Ha, swiglu, s));
     BwdGemmLaunch g2 = bwd_gemm(act, Ha, 1, false, w->w2, Ha, 1, 1ll * D * Ha, bf, o, D, pairs, Ha, D);
     g2.offsets = offsets; g2.G = M;
@@ -1436,7 +1685,12 @@ moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, co
     float* hs = at<float*>(ws, L.hs);
     float* as = at<float*>(ws, L.as);
     float* das = at<float*>(ws, L.das);
-    MOE_CUDA(launch_bwd_gemm(bwd_gemm(x, D, 1, bf, w->sh_w1, D, 1, 0, bf, hs, 2 * Is, T, D, 2 * Is), s));
+    if (ckpt == nullptr) {
+      MOE_CUDA(launch_bwd_gemm(bwd_gemm(x, D, 1, bf, w->sh_w1, D, 1, 0, bf, hs, 2 * Is, T, D, 2 * Is), s));
+    } else {
+      MOE_CUDA(launch_ckpt_dequantize(MOE_DTYPE_F32, at<int8_t*>(ckpt, C.sq), at<uint8_t*>(ckpt, C.se), nullptr,
+                                      nullptr, 2 * T, 2 * T, Is, hs, status, s));
+    }
     MOE_CUDA(launch_bwd_act(hs, as, nullptr, T, Is, true, s));
     MOE_CUDA(launch_bwd_gemm(bwd_gemm(dy, D, 1, bf, w->sh_w2, 1, Is, 0, bf, das, Is, T, D, Is), s));
     MOE_CUDA(launch_bwd_act_grad(das, hs, nullptr, T, Is, true, s));
@@ -1464,6 +1718,41 @@ moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, co
     MOE_CUDA(launch_combine(d->dtype, dxp, slot_of, dxs, true, nullptr, g->dx, T, D, k, s));
   }
   return MOE_OK;
+}
+
+
+// ckpt (may be null): moe_backward_saved, which reads the routing and the
+// pre-activations there.
+moe_status_t backward_impl(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
+                           const moe_grads_t* g, void* ws, size_t ws_bytes, cudaStream_t s, void* ckpt = nullptr) {
+  MOE_TRY(check_desc(d));
+  MOE_TRY(check_weights(d, w, true, true));
+  if (w->w_r == nullptr || g == nullptr) return MOE_ERR_INVALID_ARG;
+  const bool swiglu = d->act == MOE_ACT_SWIGLU;
+  const bool biases = !swiglu && d->has_bias;
+  if (!g->dw_r || !g->dw1 || !g->dw2) return MOE_ERR_INVALID_ARG;
+  if (biases && (!g->db1 || !g->db2)) return MOE_ERR_INVALID_ARG;
+  if (d->I_sh > 0 && (!g->dsh_w1 || !g->dsh_w2)) return MOE_ERR_INVALID_ARG;
+  if (d->T == 0) {
+    MOE_TRY(check_device());
+    return zero_param_grads(d, g, s);
+  }
+  if (!x || !dy || !g->dx || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
+  if (d->dtype == MOE_DTYPE_BF16) {
+    if (!al16(x) || !al16(dy) || !al16(w->w_r) || !al16(g->dw1) || !al16(g->dw2)) return MOE_ERR_INVALID_ARG;
+    if (d->I_sh > 0 && (!al16(g->dsh_w1) || !al16(g->dsh_w2))) return MOE_ERR_INVALID_ARG;
+  }
+  if (ckpt != nullptr) {
+    if (ws_bytes < saved_layout(d).total) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_device());
+    if (d->dtype == MOE_DTYPE_BF16) return saved_backward_tc(d, w, x, dy, ckpt, g, ws, s);
+    return backward_f32(d, w, x, dy, g, ws, saved_f32_ws(d), ckpt, s);
+  }
+  const BwdWs L = backward_layout(d);
+  if (ws_bytes < L.total) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  if (d->dtype == MOE_DTYPE_BF16) return backward_tc_impl(d, w, x, dy, g, ws, s);
+  return backward_f32(d, w, x, dy, g, ws, plain_f32_ws(L), nullptr, s);
 }
 
 }  // namespace
@@ -1503,6 +1792,60 @@ int moe_backward_launch_count(const moe_layer_desc_t* d) {
   n += 3;                                                            // router backward, dW_r, router dx
   n += 1;                                                            // dx combine
   return n;
+}
+
+// ------------------------------------------------- training with a checkpoint
+
+size_t moe_checkpoint_size(const moe_layer_desc_t* d) { return check_desc(d) == MOE_OK ? ckpt_layout(d).total : 0; }
+
+moe_status_t moe_checkpoint_offsets(const moe_layer_desc_t* d, size_t* out) {
+  MOE_TRY(check_desc(d));
+  if (out == nullptr) return MOE_ERR_INVALID_ARG;
+  const CkptLayout C = ckpt_layout(d);
+  const size_t parts[MOE_CHECKPOINT_PARTS] = {C.idx, C.tw, C.logits, C.q, C.e, C.sq, C.se};
+  std::copy(parts, parts + MOE_CHECKPOINT_PARTS, out);
+  return MOE_OK;
+}
+
+// The forward's workspace and, for fp32 layers, room for the pre-activations.
+static size_t forward_save_ws(const moe_layer_desc_t* d, size_t* h_at) {
+  *h_at = align_up(forward_layout(d).pub.total);
+  if (d->dtype == MOE_DTYPE_BF16) return *h_at;
+  const size_t n1 = d->act == MOE_ACT_SWIGLU ? 2ull * d->I : static_cast<size_t>(d->I), T = d->T;
+  return *h_at + align_up(std::max(T * d->k * n1, T * 2 * d->I_sh) * 4);
+}
+
+size_t moe_forward_save_workspace_size(const moe_layer_desc_t* d) {
+  size_t at_h;
+  return check_desc(d) == MOE_OK ? forward_save_ws(d, &at_h) : 0;
+}
+
+moe_status_t moe_forward_save(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* addend,
+                              void* y, void* ckpt, size_t ckpt_bytes, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_desc(d));
+  if (d->T > 0) {
+    size_t at_h;
+    if (!ckpt || !aligned_ws(ckpt) || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
+    if (ckpt_bytes < ckpt_layout(d).total || ws_bytes < forward_save_ws(d, &at_h)) return MOE_ERR_INVALID_ARG;
+    const CkptLayout C = ckpt_layout(d);
+    const Keep keep = {at<int8_t*>(ckpt, C.q), at<uint8_t*>(ckpt, C.e), at<int8_t*>(ckpt, C.sq),
+                       at<uint8_t*>(ckpt, C.se), at<float*>(ws, at_h)};
+    return forward_impl(d, w, x, addend, y, ws, ws_bytes, static_cast<cudaStream_t>(stream), nullptr, ckpt, &keep);
+  }
+  return forward_impl(d, w, x, addend, y, ws, ws_bytes, static_cast<cudaStream_t>(stream), nullptr);
+}
+
+size_t moe_backward_saved_workspace_size(const moe_layer_desc_t* d) {
+  return check_desc(d) == MOE_OK ? saved_layout(d).total : 0;
+}
+
+moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
+                                const void* ckpt, size_t ckpt_bytes, const moe_grads_t* grads, void* ws,
+                                size_t ws_bytes, void* stream) {
+  MOE_TRY(check_desc(d));
+  if (d->T > 0 && (!ckpt || !aligned_ws(ckpt) || ckpt_bytes < ckpt_layout(d).total)) return MOE_ERR_INVALID_ARG;
+  return backward_impl(d, w, x, dy, grads, ws, ws_bytes, static_cast<cudaStream_t>(stream),
+                       const_cast<void*>(ckpt));
 }
 
 }  // extern "C"

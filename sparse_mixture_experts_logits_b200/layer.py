@@ -59,6 +59,38 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+class LayerCheckpoint:
+    """What one forward of ``layer`` keeps for its backward: the routing, and
+    the pre-activations in 8 bits.  Holds for one forward at a time; a step
+    that keeps several (gradient accumulation over overlapping micro-batches)
+    takes one each."""
+
+    def __init__(self, layer: "MoELayer"):
+        self.nbytes = abi.moe_checkpoint_size(layer.desc)
+        if self.nbytes == 0 and layer.desc.T > 0:
+            raise abi.MoEError("moe_checkpoint_size", abi.MOE_ERR_INVALID_ARG)
+        self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=layer.device)
+        self._off = (-self.buffer.data_ptr()) % 256
+        self.ptr = self.buffer.data_ptr() + self._off
+        self.desc = layer.desc
+
+    def view(self, name: str) -> torch.Tensor:
+        """A part of the checkpoint as a tensor: "topk_idx", "topk_w" [T, k],
+        "logits" [T, M], "q", "e" (the routed experts' pre-activations, rows
+        in dispatch order) or "shared_q", "shared_e"."""
+        d = self.desc
+        halves = 2 if d.act == abi.ACT_SWIGLU else 1
+        shapes = {"topk_idx": ((d.T, d.k), torch.int32), "topk_w": ((d.T, d.k), torch.float32),
+                  "logits": ((d.T, d.M), torch.float32), "q": ((d.T * d.k, halves * d.I), torch.int8),
+                  "e": ((d.T * d.k, halves * abi.moe_ckpt_blocks(d.I)), torch.uint8),
+                  "shared_q": ((d.T, 2 * d.I_sh), torch.int8),
+                  "shared_e": ((d.T, 2 * abi.moe_ckpt_blocks(d.I_sh)), torch.uint8)}
+        shape, dt = shapes[name]
+        off = self._off + abi.moe_checkpoint_offsets(d)[list(shapes).index(name)]
+        nbytes = shape[0] * shape[1] * torch.empty((), dtype=dt).element_size()
+        return self.buffer[off:off + nbytes].view(dt).view(shape)
+
+
 class MoELayer:
     """One MoE layer bound to device weight tensors (kept alive here)."""
 
@@ -76,16 +108,29 @@ class MoELayer:
         self._ws_off = (-base) % 256
         self.layout = abi.moe_workspace_layout(self.desc)
         self._bws = None
+        self._save = None
+        self._cws = None
+        self._last_bws = None
 
     @property
     def ws_ptr(self) -> int:
         return self.ws.data_ptr() + self._ws_off
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None,
-                addend: torch.Tensor | None = None) -> torch.Tensor:
-        """y = MoE-FFN(x), or addend + MoE-FFN(x) when ``addend`` is given."""
+                addend: torch.Tensor | None = None, checkpoint: LayerCheckpoint | None = None) -> torch.Tensor:
+        """y = MoE-FFN(x), or addend + MoE-FFN(x) when ``addend`` is given.
+        With ``checkpoint`` the pass also keeps there what
+        ``backward(..., checkpoint=...)`` needs (moe_forward_save)."""
         if y is None:
             y = torch.empty_like(x)
+        if checkpoint is not None:
+            if self._save is None:
+                nbytes = abi.moe_forward_save_workspace_size(self.desc)
+                # a bf16 layer keeps them from its own workspace
+                self._save = (self.ws_ptr, self.ws_bytes, None) if nbytes <= self.ws_bytes else self._scratch(nbytes)
+            abi.moe_forward_save(self.desc, self.weights, x.data_ptr(), _ptr(addend), y.data_ptr(), checkpoint.ptr,
+                                 checkpoint.nbytes, self._save[0], self._save[1], _stream_handle(stream))
+            return y
         if addend is None:
             abi.moe_forward(self.desc, self.weights, x.data_ptr(), y.data_ptr(), self.ws_ptr, self.ws_bytes,
                             _stream_handle(stream))
@@ -93,6 +138,11 @@ class MoELayer:
             abi.moe_forward_add(self.desc, self.weights, x.data_ptr(), addend.data_ptr(), y.data_ptr(),
                                 self.ws_ptr, self.ws_bytes, _stream_handle(stream))
         return y
+
+    def _scratch(self, nbytes: int):
+        """(256-byte aligned address, bytes, buffer)"""
+        buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
+        return buf.data_ptr() + (-buf.data_ptr()) % 256, nbytes, buf
 
     def device_status(self, stream=None) -> int:
         return abi.moe_device_status(self.ws_ptr, _stream_handle(stream))
@@ -109,12 +159,16 @@ class MoELayer:
             "dsh_w1": (2 * d.I_sh, d.D) if d.I_sh else None, "dsh_w2": (d.D, d.I_sh) if d.I_sh else None,
         }
 
-    def backward(self, x: torch.Tensor, dy: torch.Tensor, grads: dict | None = None, stream=None) -> dict:
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, grads: dict | None = None, stream=None,
+                 checkpoint: LayerCheckpoint | None = None) -> dict:
         """Gradients of L = sum(dy * MoE-FFN(x)) (moe_backward): dx in the
         layer's dtype, every parameter gradient in fp32.  The backward has its
         own workspace (allocated on first use); ``backward_view`` reads the
-        routing it recomputed."""
-        if self._bws is None:
+        routing it recomputed.  With the ``checkpoint`` of a forward on the
+        same x nothing of that forward is recomputed (moe_backward_saved)."""
+        if checkpoint is not None and self._cws is None:
+            self._cws = self._scratch(abi.moe_backward_saved_workspace_size(self.desc))
+        if checkpoint is None and self._bws is None:
             self.bws_bytes = abi.moe_backward_workspace_size(self.desc)
             if self.bws_bytes == 0:
                 raise abi.MoEError("moe_backward_workspace_size", abi.MOE_ERR_INVALID_ARG)
@@ -129,12 +183,19 @@ class MoELayer:
         g = abi.Grads()
         for name in abi.Grads._fields_:
             setattr(g, name[0], _ptr(grads.get(name[0])))
-        abi.moe_backward(self.desc, self.weights, x.data_ptr(), dy.data_ptr(), g,
-                         self._bws.data_ptr() + self._bws_off, self.bws_bytes, _stream_handle(stream))
+        if checkpoint is not None:
+            self._last_bws = self._cws[0]
+            abi.moe_backward_saved(self.desc, self.weights, x.data_ptr(), dy.data_ptr(), checkpoint.ptr,
+                                   checkpoint.nbytes, g, self._cws[0], self._cws[1], _stream_handle(stream))
+            return grads
+        self._last_bws = self._bws.data_ptr() + self._bws_off
+        abi.moe_backward(self.desc, self.weights, x.data_ptr(), dy.data_ptr(), g, self._last_bws, self.bws_bytes,
+                         _stream_handle(stream))
         return grads
 
     def backward_status(self, stream=None) -> int:
-        return abi.moe_device_status(self._bws.data_ptr() + self._bws_off, _stream_handle(stream))
+        """The status of the last backward."""
+        return abi.moe_device_status(self._last_bws, _stream_handle(stream))
 
     def backward_view(self, name: str) -> torch.Tensor:
         """The routing intermediate ``name`` of the last backward."""

@@ -107,3 +107,34 @@ def test_handles_refuse_on_the_host(moe):
         moe.RowCheckpoint(4, 8, torch.float32, device="cpu")
     with pytest.raises(ValueError, match="act"):
         moe.ActivationCheckpoint("relu", 4, 8, torch.float32)
+
+
+def _layer(moe, **over):
+    import moe_synth as ms
+    d = moe.desc_from_config(ms.get_config("glm_small_bf16", **over))
+    w = moe.Weights()
+    w.w_r, w.w1, w.w2, w.sh_w1, w.sh_w2 = P, P, P, P, P
+    return d, w, moe.Grads(dx=P, dw_r=P, dw1=P, dw2=P, dsh_w1=P, dsh_w2=P)
+
+
+def test_layer_checkpoint_refuses(moe):
+    d, w, g = _layer(moe)
+    ck, fs, bs = moe.moe_checkpoint_size(d), moe.moe_forward_save_workspace_size(d), moe.moe_backward_saved_workspace_size(d)
+    pairs, blocks = d.T * d.k, -(-d.I // 32)
+    assert ck >= pairs * (2 * d.I + 2 * blocks + 8) + d.T * (4 * d.M + 2 * d.I_sh)
+    assert fs >= moe.moe_workspace_size(d) and 0 < bs < moe.moe_backward_workspace_size(d)
+    offs = moe.moe_checkpoint_offsets(d)
+    assert offs == sorted(offs) and all(o % 256 == 0 for o in offs) and offs[-1] < ck
+    for args in [(None, ck, P, fs), (P + 8, ck, P, fs), (P, ck - 1, P, fs), (P, ck, None, fs), (P, ck, P, fs - 1), (P, ck, P + 8, fs)]:
+        assert _status(moe, moe.moe_forward_save, d, w, P, None, P, *args) == 1, args
+    assert _status(moe, moe.moe_forward_save, d, w, None, None, P, P, ck, P, fs) == 1
+    for args in [(None, ck, g, P, bs), (P + 8, ck, g, P, bs), (P, ck - 1, g, P, bs), (P, ck, g, None, bs),
+                 (P, ck, g, P, bs - 1), (P, ck, moe.Grads(dx=P, dw_r=P, dw1=P), P, bs)]:
+        assert _status(moe, moe.moe_backward_saved, d, w, P, P, *args) == 1, args
+    bad, _, _ = _layer(moe)
+    bad.k = 0
+    for fn in (moe.moe_checkpoint_size, moe.moe_forward_save_workspace_size, moe.moe_backward_saved_workspace_size):
+        assert fn(bad) == 0
+    assert _status(moe, moe.moe_checkpoint_offsets, bad) == 1
+    zero, w, _ = _layer(moe, T=0)
+    moe.moe_forward_save(zero, w, None, None, None, None, 0, None, 0)
