@@ -311,37 +311,77 @@ __device__ __forceinline__ float warp_transpose_sum(float (&v)[32], int lane) {
   return v[0];
 }
 
+// The four lanes of a quad exchange a 4 x 4 matrix of bytes: lane j's word t
+// byte i becomes lane i's byte j (its own inverse).
+__device__ __forceinline__ uint32_t transpose_bytes4(uint32_t p, int lane) {
+  const uint32_t p1 = __shfl_xor_sync(0xffffffffu, p, 1);
+  const uint32_t x = __byte_perm(p, p1, (lane & 1) ? 0x3715 : 0x6240);
+  const uint32_t x2 = __shfl_xor_sync(0xffffffffu, x, 2);
+  return __byte_perm(x, x2, (lane & 2) ? 0x3276 : 0x5410);
+}
+
 // Keeps 32 rows (r[i]: row `row` + i of this lane's column `col`; the warp's
 // lanes are 32 consecutive columns, i.e. one block) of half `half` in 8 bits.
-// Four rows at a time: the block's exponent is a warp-wide maximum, and the
-// four lanes of a quad transpose their 4 x 4 bytes, so that lane j stores row
-// j's four columns as one word.  half_cols is a multiple of 16.
+// Four rows at a time: the block's exponent is a warp-wide maximum, one fused
+// multiply-add scales and rounds (what it does not cover is done again the
+// long way, as in ckpt.cu), and the quad transposes its bytes, so that lane j
+// stores row j's four columns as one word.  half_cols is a multiple of 16.
 __device__ __forceinline__ void keep_rows32(const SwapArgs& a, const float (&r)[32], size_t row, int nv, int col,
                                             bool col_ok, int halves, int half, int lane) {
   const int j = lane & 3;
   int8_t* qp = a.keep_q + ((row + j) * halves + half) * a.half_cols + (col & ~3);
   uint8_t* ep = a.keep_e + ((row + lane) * halves + half) * a.keep_blocks + ((col - lane) >> 5);
-  const size_t q4 = static_cast<size_t>(4 * halves) * a.half_cols, e4 = static_cast<size_t>(4 * halves) * a.keep_blocks;
+  const size_t q4 = static_cast<size_t>(4 * halves) * a.half_cols;
   const bool any = col - lane < a.half_cols;
+  uint32_t mine = 0;  // the exponent of row `lane`
 #pragma unroll
-  for (int i = 0; i < 32; i += 4, qp += q4, ep += e4) {
-    uint32_t b[4], mine = 0;
+  for (int i = 0; i < 32; i += 4, qp += q4) {
+    uint32_t b[4], e[4];
+    bool odd = false;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const float v = col_ok ? r[i + t] : 0.f;
-      const uint32_t e = __reduce_max_sync(0xffffffffu, abs_bits(v)) >> 23;
-      const float u = fminf(fmaxf(v * ckpt_inv_scale(e), -127.0f / 64.0f), 127.0f / 64.0f);
-      b[t] = e == 255u ? 0u : __float_as_uint(fmaf(u, 64.0f, 12582912.0f));
-      if (lane == t) mine = e;
+      e[t] = __reduce_max_sync(0xffffffffu, abs_bits(v)) >> 23;
+      b[t] = __float_as_uint(fmaf(v, __uint_as_float((260u - e[t]) << 23), 12582912.0f));
+      odd |= e[t] - 6u > 248u;
+      if (lane == i + t) mine = e[t];
     }
-    const uint32_t p = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    const uint32_t p1 = __shfl_xor_sync(0xffffffffu, p, 1);
-    const uint32_t x = __byte_perm(p, p1, (j & 1) ? 0x3715 : 0x6240);
-    const uint32_t x2 = __shfl_xor_sync(0xffffffffu, x, 2);
-    const uint32_t word = __byte_perm(x, x2, (j & 2) ? 0x3276 : 0x5410);
+    uint32_t p = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    const uint32_t x = p ^ 0x80808080u;  // a zero byte where a value rounds to +-128
+    odd |= (((x - 0x01010101u) & ~x) & 0x80808080u) != 0u;
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float u = (col_ok ? r[i + t] : 0.f) * ckpt_inv_scale(e[t]);
+        b[t] = __float_as_uint(fmaf(fminf(fmaxf(u, -127.0f / 64.0f), 127.0f / 64.0f), 64.0f, 12582912.0f));
+        if (e[t] == 255u) b[t] = 0u;
+      }
+      p = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    const uint32_t word = transpose_bytes4(p, lane);
     if (col_ok && i + j < nv) *reinterpret_cast<uint32_t*>(qp) = word;
-    if (any && lane < 4 && i + lane < nv) *ep = static_cast<uint8_t>(mine);
   }
+  if (any && lane < nv) *ep = static_cast<uint8_t>(mine);
+}
+
+// The way back: eight words (lane j: rows j, 4 + j, ...) and the exponent of
+// row `lane`, loaded before anything waits for them; then row i's value of
+// this lane's column (`scale`: ckpt_scale of row `lane`'s exponent).
+__device__ __forceinline__ void keep_load32(const SwapArgs& a, size_t row, int nv, int col, bool col_ok, int halves,
+                                            int half, int lane, uint32_t (&w)[8], uint32_t& e) {
+  const int j = lane & 3;
+  const int8_t* qp = a.keep_q + ((row + j) * halves + half) * a.half_cols + (col & ~3);
+  const size_t q4 = static_cast<size_t>(4 * halves) * a.half_cols;
+#pragma unroll
+  for (int t = 0; t < 8; ++t, qp += q4)
+    w[t] = col_ok && 4 * t + j < nv ? *reinterpret_cast<const uint32_t*>(qp) : 0u;
+  e = col - lane < a.half_cols && lane < nv
+          ? a.keep_e[((row + lane) * halves + half) * a.keep_blocks + ((col - lane) >> 5)]
+          : 0u;
+}
+__device__ __forceinline__ float keep_value(uint32_t word, int i, float scale) {
+  const float f = __uint_as_float(__byte_perm(word ^ 0x80808080u, 0x4B000000u, 0x7440 + (i & 3))) - 8388736.0f;
+  return f * __shfl_sync(0xffffffffu, scale, i);
 }
 
 template <int EPI, int LAYOUT>
@@ -907,20 +947,19 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         // they would wait one memory round trip per row: the compiler cannot
         // move a load above the store to `out` before it.
         float hv[32], uv[32];
-        if constexpr (kDact || EPI == EPI_BIAS_ADD) {
+        uint32_t hw[8], uw[8], he = 0, ue = 0;
+        if constexpr (kKeptDact) {
+          constexpr int kHalves = kDactSwiglu ? 2 : 1;
+          const int nvd = min(32, t.nrows - c);
+          keep_load32(args, row0 + c, nvd, col, col_ok, kHalves, 0, lane, hw, he);
+          if constexpr (kDactSwiglu) keep_load32(args, row0 + c, nvd, col, col_ok, kHalves, 1, lane, uw, ue);
+        } else if constexpr (kDact || EPI == EPI_BIAS_ADD) {
           const int nvd = min(32, t.nrows - c);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const bool live = col_ok && i < nvd;
             const size_t row = row0 + c + i;
-            if constexpr (kKeptDact) {
-              constexpr int kHalves = kDactSwiglu ? 2 : 1;
-              const int8_t* qr = args.keep_q + row * kHalves * args.half_cols + col;
-              const uint8_t* er = args.keep_e + row * kHalves * args.keep_blocks + (col >> 5);
-              hv[i] = live ? static_cast<float>(qr[0]) * ckpt_scale(er[0]) : 0.f;
-              if constexpr (kDactSwiglu)
-                uv[i] = live ? static_cast<float>(qr[args.half_cols]) * ckpt_scale(er[args.keep_blocks]) : 0.f;
-            } else if constexpr (kDact) {
+            if constexpr (kDact) {
               hv[i] = live ? args.aux[row * args.ld_aux + col] : 0.f;
               if constexpr (EPI == EPI_BWD_SWIGLU_DACT)
                 uv[i] = live ? args.aux[row * args.ld_aux + args.half_cols + col] : 0.f;
@@ -1016,6 +1055,20 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           }
           keep_rows32(args, v, row0 + c, nv, col, col_ok, 1, 0, lane);
         } else if constexpr (kDact) {
+          if constexpr (kKeptDact) {
+            const float hs = ckpt_scale(he), us = ckpt_scale(ue);
+#pragma unroll
+            for (int t4 = 0; t4 < 8; ++t4) {
+              const uint32_t a4 = transpose_bytes4(hw[t4], lane);
+              uint32_t b4 = 0;
+              if constexpr (kDactSwiglu) b4 = transpose_bytes4(uw[t4], lane);
+#pragma unroll
+              for (int i = 4 * t4; i < 4 * t4 + 4; ++i) {
+                hv[i] = keep_value(a4, i, hs);
+                if constexpr (kDactSwiglu) uv[i] = keep_value(b4, i, us);
+              }
+            }
+          }
           // G = acc (the gradient reaching a, before the gate weight); dh out,
           // and per token the partial <G, a> over this warp's 32 columns
           float prod[32];

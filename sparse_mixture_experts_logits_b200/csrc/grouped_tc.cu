@@ -21,8 +21,7 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // go to tail[g * 64 ..]; a group without rows gets its `out` zeroed unless it
 // is added onto.  blockIdx.x shares the 16-byte units of each; blockIdx.z
 // picks the operand.  Blocks of blockIdx.z = 2 take db's column sums when
-// they fit one block per 64 columns and group (a launch saved), and the first
-// block clears the status word.
+// they are few (a launch saved), and the first block clears the status word.
 __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restrict__ x, const uint4* __restrict__ dy,
                                                             const int32_t* __restrict__ offsets, int rows, int vk,
                                                             int vn, long long out_units, int accumulate,
@@ -83,7 +82,9 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     const long long units = static_cast<long long>(L.N) * L.K / 4;
     const long long most = std::max<long long>(kTail * static_cast<long long>(std::max(vk, vn)), units / 2);
     const int share = static_cast<int>(std::max<long long>(1, std::min<long long>((most + 1023) / 1024, 32)));
-    const bool sums = L.db != nullptr && grouped_colsum_shares(L.G, L.rows, L.N) == 1;
+    // the sums beside the preparation when they are a wave of blocks at most (16384 x 8192: 76 us there, 51 apart)
+    const bool sums = L.db != nullptr && grouped_colsum_shares(L.G, L.rows, L.N) == 1 &&
+                      static_cast<long long>((L.N + 63) / 64) * L.G <= 4 * num_sms();
     wgrad_prepare_kernel<<<dim3(share, L.G, sums ? 3 : 2), 256, 0, s>>>(
         static_cast<const uint4*>(L.x), static_cast<const uint4*>(L.dy), L.offsets, L.rows, vk, vn, units,
         L.accumulate, reinterpret_cast<uint4*>(x_tail), reinterpret_cast<uint4*>(dy_tail), static_cast<uint4*>(L.out),
