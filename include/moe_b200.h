@@ -532,9 +532,10 @@ moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* 
  *          terms at a time when the output is fp32, the parts added in fp32
  *          with rounding.  Fixed order: the same call gives the same bits.
  * bf16 runs on the tensor cores when N and K are multiples of 8 (else on the
- * CUDA cores) and then needs x, dy, w and dw on 16-byte boundaries; fp32 runs
- * on the CUDA cores.  Tensors must not overlap.  Limits: G <= 1024,
- * G N K < 2^40, rows, N, K < 2^30.  rows = 0 is valid. */
+ * CUDA cores) and then needs x, dy, w, y, dx and dw on 16-byte boundaries
+ * (MOE_ERR_INVALID_ARG otherwise); fp32 runs on the CUDA cores.  Tensors must
+ * not overlap.  Limits: G <= 1024, G N K < 2^40, rows < 2^30, N, K < 2^24.
+ * rows = 0 is valid. */
 
 /* Workspace of moe_grouped_gemm and moe_grouped_dgrad; 0 if an argument is
  * invalid. */
@@ -574,9 +575,9 @@ moe_status_t moe_grouped_wgrad(const void* x, const void* dy, const int32_t* off
  * a NaN or an infinity (e = 255) reads back as NaN throughout.
  *   q int8 [rows, cols], e uint8 [rows, moe_ckpt_blocks(cols)].
  * n_rows (device int32, or NULL for all `rows`) limits the rows that are
- * read and written; the others stay as they were.  Any width; widths that
- * are a multiple of 8 with every tensor on a 16-byte boundary are the fast
- * ones. */
+ * read and written; the others stay as they were.  Any width and alignment;
+ * widths that are a multiple of 8 with every tensor on a 16-byte boundary are
+ * the fast ones.  Tensors must not overlap.  Limits: rows, cols, I < 2^30. */
 #define MOE_CKPT_BLOCK 32
 
 /* Blocks of a row of `cols` values: ceil(cols / MOE_CKPT_BLOCK). */

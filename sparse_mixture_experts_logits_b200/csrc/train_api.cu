@@ -10,8 +10,7 @@ moe_status_t check_grouped(int G, int N, int K, int rows, int dtype) {
   if (G < 1 || N < 1 || K < 1 || rows < 0) return MOE_ERR_INVALID_ARG;
   if (!is_dtype(dtype) || G > kMaxExperts) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * K >= (1ll << 40) / G) return MOE_ERR_UNSUPPORTED;
-  if (rows >= (1 << 30) || static_cast<long long>(N) >= (1 << 30) || static_cast<long long>(K) >= (1 << 30))
-    return MOE_ERR_UNSUPPORTED;
+  if (rows >= (1 << 30) || N >= (1 << 24) || K >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -52,7 +51,7 @@ moe_status_t check_rows_call(const void* a, const void* w, const int32_t* offset
   MOE_TRY(check_out(dtype, out_dtype));
   if (rows == 0) return MOE_OK;
   if (!a || !w || !offsets || !out || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
-  if (grouped_tc_ok(dtype, N, K) && (!al16(a) || !al16(w))) return MOE_ERR_INVALID_ARG;
+  if (grouped_tc_ok(dtype, N, K) && (!al16(a) || !al16(w) || !al16(out))) return MOE_ERR_INVALID_ARG;
   return ws_bytes < grouped_ws(kGroupedFwd, G, N, K, dtype) ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 

@@ -2,7 +2,7 @@
 products grouped by expert (GroupedLinear) and the 8-bit activation
 checkpoints (RowCheckpoint, ActivationCheckpoint).  Each checks its tensors,
 holds its workspace or checkpoint and calls the C ABI; no computation happens
-here.
+here, and nothing is recorded for autograd.
 
 Every call runs on ``stream``, or on the current stream of the handle's device
 when none is given (the caller keeps tensors made on another stream alive and

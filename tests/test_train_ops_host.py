@@ -43,7 +43,8 @@ def _wgrad(moe, **kw):
 
 BAD = [(dict(G=0), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(rows=-1), 1), (dict(dtype=5), 2), (dict(G=1025), 2),
        (dict(N=1 << 20, K=1 << 20), 2), (dict(rows=1 << 30), 2), (dict(x=None), 1), (dict(offsets=None), 1),
-       (dict(y=None), 1), (dict(ws=None), 1), (dict(ws=P + 8), 1), (dict(n=0), 1)]
+       (dict(y=None), 1), (dict(ws=None), 1), (dict(ws=P + 8), 1), (dict(n=0), 1), (dict(x=P + 8), 1), (dict(y=P + 2), 1),
+       (dict(K=1 << 24, N=8), 2)]
 
 
 @pytest.mark.parametrize("kw,status", BAD)
@@ -57,7 +58,9 @@ def test_grouped_rows_products_refuse(moe):
         assert _status(moe, *call(moe, w=None)) == 1
         assert _status(moe, *call(moe, out=7)) == 2
         assert _status(moe, *call(moe, dtype=0, out=1)) == 2      # fp32 in, bf16 out
-    assert _status(moe, *_wgrad(moe, dy=None)) == 1
+        assert _status(moe, *call(moe, w=P + 4)) == 1
+    for dy in (None, P + 4):
+        assert _status(moe, *_wgrad(moe, dy=dy)) == 1
 
 
 def test_workspace_queries(moe):

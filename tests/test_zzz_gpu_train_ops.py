@@ -143,6 +143,122 @@ def test_offsets_that_are_no_dispatch_stay_inside(moe, dtype):
     _close(db, wb, (rows + 8) * 2.0 ** -24 * mb, "db")
 
 
+def test_as_many_experts_as_there_can_be(moe):
+    """1024 experts of zero to three rows."""
+    counts = np.arange(1024) * 7 % 4
+    offsets, N, K = _offsets(counts), 24, 40
+    rows = int(offsets[-1])
+    x, dy, w = _randn(1, (rows, K), torch.bfloat16), _randn(2, (rows, N), torch.bfloat16), _randn(3, (1024, N, K), torch.bfloat16)
+    op = moe.GroupedLinear(w, rows, out_dtype=torch.float32)
+    off = _dev(offsets)
+    want, m = ref.grouped_gemm(np64(x), np64(w), None, offsets, np.zeros((rows, N)))
+    _close(op.forward(x, off), want, ref.gamma(K, "f32") * m, "y")
+    dw, db = op.weight_grad(x, dy, off, db=True)
+    ww, wb, mw, mb = ref.grouped_wgrad(np64(x), np64(dy), offsets)
+    _close(dw, ww, ref.gamma(3, "f32") * mw, "dw")
+    _close(db, wb, 11 * 2.0 ** -24 * mb, "db")
+    with pytest.raises(moe.MoEError):
+        moe.GroupedLinear(_randn(3, (1025, 8, 8), torch.bfloat16), rows)
+
+
+def test_rows_behind_two_billion_elements(moe):
+    """Element offsets past 32 bits, in the rows and in the segments."""
+    K, N, rows = 8192, 16, 270_000
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    w = _randn(3, (2, N, K), torch.bfloat16, K ** -0.5)
+    offsets = [0, rows - 100, rows - 3]
+    op = moe.GroupedLinear(w, rows, out_dtype=torch.float32)
+    off = _dev(offsets)
+    y = op.forward(x, off, y=torch.full((rows, N), 7.0, device="cuda"))
+    for r in (0, 262_143, 262_145, rows - 101, rows - 100, rows - 4):
+        want = np64(x[r]) @ np64(w[int(r >= offsets[1])]).T
+        m = np.abs(np64(x[r])) @ np.abs(np64(w[int(r >= offsets[1])])).T
+        _close(y[r], want, ref.gamma(K, "f32") * m, f"y[{r}]")
+    assert y[rows - 3:].eq(7).all()
+    dy = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+    dy[rows - 50, 3] = 1.0
+    dw, _ = op.weight_grad(x, dy, off)
+    assert not dw[0].any() and torch.equal(dw[1, 3], x[rows - 50].float())
+    dy = _randn(4, (rows, N), torch.bfloat16)
+    dx = moe.GroupedLinear(w, rows).input_grad(dy, off)
+    want = np64(dy[rows - 4]) @ np64(w[1])
+    m = np.abs(np64(dy[rows - 4])) @ np.abs(np64(w[1]))
+    _close(dx[rows - 4], want, ref.gamma(N, "bf16") * m + ref.U["bf16"] * np.abs(want), "dx")
+    c = moe.RowCheckpoint(rows, K, torch.bfloat16)
+    c.save(x)
+    idx = torch.tensor([rows - 1, 262_145], dtype=torch.int32, device="cuda")
+    assert np.array_equal(np64(c.load(idx)), ref.keep(np64(x[idx.long()]))[2])
+    ck = moe.ActivationCheckpoint("gelu_tanh", rows, K, torch.bfloat16)
+    a = ck.save(x)
+    last = np64(x[-1:])
+    _close(a[-1:], ref.act(last, False)[0], ref.act(last, False)[1] + ref.U["bf16"] * np.abs(last) + 1e-36, "a")
+    dh, _, _ = ck.backward(a)
+    v = ref.keep(last)[2]
+    d, bd = ref.act_grad(v, False)
+    ga = np64(a[-1:])
+    _close(dh[-1:], ga * d, np.abs(ga) * bd + ref.U["bf16"] * np.abs(ga * d) + 1e-36, "dh")
+
+
+def test_what_the_handles_refuse(moe):
+    w = _randn(1, (2, 16, 24), torch.bfloat16)
+    op = moe.GroupedLinear(w, 4)
+    x, off = _randn(2, (4, 24), torch.bfloat16), _dev([0, 1, 4])
+    odd = torch.zeros(4 * 24 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 24)   # contiguous, off its boundary
+    for bad in (x.float(), x[:3], x.cpu(), _randn(2, (24, 4), torch.bfloat16).t()):
+        with pytest.raises(ValueError, match="x must be"):
+            op.forward(bad, off)
+    with pytest.raises(ValueError, match="offsets"):
+        op.forward(x, off.long())
+    with pytest.raises(ValueError, match="y must be"):
+        op.forward(x, off, y=torch.empty(4, 16, device="cuda"))
+    with pytest.raises(moe.MoEError):
+        op.forward(odd, off)
+    with pytest.raises(ValueError, match="accumulate"):
+        op.weight_grad(x, _randn(3, (4, 16), torch.bfloat16), off, accumulate=True)
+    with pytest.raises(ValueError, match="bias"):
+        moe.GroupedLinear(w, 4, bias=torch.zeros(2, 16, device="cuda"))
+    with pytest.raises(ValueError, match="weight"):
+        moe.GroupedLinear(w.transpose(1, 2), 4)
+    with pytest.raises(ValueError, match="dtype"):
+        moe.GroupedLinear(w.half(), 4)
+    with pytest.raises(moe.MoEError):
+        moe.GroupedLinear(w.float(), 4, out_dtype=torch.bfloat16).forward(x.float(), off)
+    ck = moe.ActivationCheckpoint("swiglu", 4, 12, torch.bfloat16)
+    with pytest.raises(ValueError, match="h must be"):
+        ck.save(_randn(1, (4, 12), torch.bfloat16))
+    with pytest.raises(ValueError, match="da must be"):
+        ck.backward(_randn(1, (4, 24), torch.bfloat16))
+    with pytest.raises(ValueError, match="q must be"):
+        moe.ActivationCheckpoint("swiglu", 4, 12, torch.bfloat16, q=torch.zeros(4, 12, dtype=torch.int8, device="cuda"))
+    c = moe.RowCheckpoint(4, 24, torch.bfloat16)
+    with pytest.raises(ValueError, match="row_index"):
+        c.load(torch.zeros(2, 2, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
+def test_checkpoints_off_their_boundaries(moe, act):
+    """Contiguous tensors that start anywhere: the same bits as on whole boundaries."""
+    rows, I = 5, 64
+    width = 2 * I if act == "swiglu" else I
+
+    def off(t):
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        b.copy_(t)
+        return b
+
+    h, da = _randn(1, (rows, width), torch.bfloat16), _randn(2, (rows, I), torch.bfloat16)
+    a1 = moe.ActivationCheckpoint(act, rows, I, torch.bfloat16)
+    a2 = moe.ActivationCheckpoint(act, rows, I, torch.bfloat16, q=off(a1.q), e=off(a1.e))
+    assert torch.equal(a1.save(h), a2.save(off(h), a=off(h[:, :I].contiguous())))
+    assert torch.equal(a1.q, a2.q) and torch.equal(a1.e, a2.e)
+    for x, y in zip(a1.backward(da, wa=True), a2.backward(off(da), dh=off(h), wa=off(da))):
+        assert (x is None and y is None) or torch.equal(x, y)
+    c1, c2 = moe.RowCheckpoint(rows, width, torch.bfloat16), moe.RowCheckpoint(rows, width, torch.bfloat16)
+    c1.save(h)
+    c2.save(off(h))
+    assert torch.equal(c1.q, c2.q) and torch.equal(c1.load(), c2.load(out=off(h)))
+
+
 def test_no_rows(moe):
     w = _randn(1, (3, 16, 24), torch.bfloat16)
     op = moe.GroupedLinear(w, 0)
