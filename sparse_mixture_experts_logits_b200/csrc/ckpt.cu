@@ -105,22 +105,70 @@ __device__ __forceinline__ void swiglu_grad(F2 g, F2 u, F2& a, F2& dg, F2& du) {
   dg = u * fma2(g, d, s);    // da / dg = u SiLU'(g)
 }
 
-// ------------------------------------------------ any width: warp per block
+// ------------------------------------------- any width and alignment
+// A warp takes kB blocks of 32 columns of a row at a time, a lane one column
+// of each: every access is a value wide, so that nothing is asked of the
+// width or the alignment, and kB (times the halves) loads are in flight.
+constexpr int kB = 8;
+
+// The kB values of this lane at columns c0 + 32 j (0 behind the row).
+template <typename T>
+__device__ __forceinline__ void load_blocks(const T* __restrict__ row, int c0, int cols, float (&v)[kB]) {
+#pragma unroll
+  for (int j = 0; j < kB; ++j) {
+    const int c = c0 + 32 * j;
+    v[j] = c < cols ? to_f32(row[c]) : 0.0f;
+  }
+}
+// Keeps them: q of the row and, lane j, the exponent of block b0 + j.
+__device__ __forceinline__ void keep_blocks(const float (&v)[kB], int c0, int cols, int b0, int nb, int lane,
+                                            int8_t* __restrict__ q, uint8_t* __restrict__ e) {
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < kB; ++j) {
+    const uint32_t ex = __reduce_max_sync(0xffffffffu, abs_bits(v[j])) >> 23;
+    if (lane == j) mine = ex;
+    const float t = fminf(fmaxf(v[j] * ckpt_inv_scale(ex), -127.0f / 64.0f), 127.0f / 64.0f);
+    const uint32_t bits = ex == 255u ? 0u : __float_as_uint(fmaf(t, 64.0f, 12582912.0f));  // see keep8
+    const int c = c0 + 32 * j;
+    if (c < cols) q[c] = static_cast<int8_t>(bits);
+  }
+  if (lane < kB && b0 + lane < nb) e[b0 + lane] = static_cast<uint8_t>(mine);
+}
+// The kept values of those columns.
+__device__ __forceinline__ void read_blocks(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, bool ok, int c0,
+                                            int cols, int b0, int nb, int lane, float (&v)[kB]) {
+  int k[kB];
+#pragma unroll
+  for (int j = 0; j < kB; ++j) k[j] = ok && c0 + 32 * j < cols ? q[c0 + 32 * j] : 0;
+  const float s = ckpt_scale(ok && lane < kB && b0 + lane < nb ? e[b0 + lane] : 0u);
+#pragma unroll
+  for (int j = 0; j < kB; ++j)
+    v[j] = (__uint_as_float(0x4B000000u + static_cast<uint32_t>(k[j] + 128)) - 8388736.0f) *
+           __shfl_sync(0xffffffffu, s, j);
+}
+
+// Unit i of a batch: `chunks` pieces of kB blocks a row.
+struct Piece { long long r; int b0, c0; };
+__device__ __forceinline__ Piece piece(long long i, int chunks, int lane) {
+  const long long r = i / chunks;
+  const int b0 = static_cast<int>(i - r * chunks) * kB;
+  return {r, b0, b0 * kBlk + lane};
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) ckpt_quantize_kernel(const T* __restrict__ src, const int32_t* n_rows, int rows,
                                                             int cols, int nb, int8_t* __restrict__ q,
                                                             uint8_t* __restrict__ e) {
-  const int lane = threadIdx.x & 31;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * nb;
+  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
+  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
   const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
        i += step) {
-    const long long r = i / nb;
-    const int c = static_cast<int>(i - r * nb) * kBlk + lane;
-    const float v = c < cols ? to_f32(src[r * cols + c]) : 0.0f;
-    const uint32_t ex = __reduce_max_sync(0xffffffffu, abs_bits(v)) >> 23;
-    if (c < cols) q[r * cols + c] = static_cast<int8_t>(ckpt_q(v, ckpt_inv_scale(ex)));
-    if (lane == 0) e[i] = static_cast<uint8_t>(ex);
+    const Piece u = piece(i, chunks, lane);
+    float v[kB];
+    load_blocks(src + u.r * cols, u.c0, cols, v);
+    keep_blocks(v, u.c0, cols, u.b0, nb, lane, q + u.r * cols, e + u.r * nb);
   }
 }
 
@@ -130,20 +178,20 @@ __global__ void __launch_bounds__(256) ckpt_dequantize_kernel(const int8_t* __re
                                                               const int32_t* __restrict__ row_index,
                                                               const int32_t* n_rows, int rows, int src_rows, int cols,
                                                               int nb, T* __restrict__ dst, int* status) {
-  const int lane = threadIdx.x & 31;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * nb;
+  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
+  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
   const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
        i += step) {
-    const long long r = i / nb;
-    const int b = static_cast<int>(i - r * nb);
-    const int c = b * kBlk + lane;
-    const long long sr = row_index != nullptr ? row_index[r] : r;
+    const Piece u = piece(i, chunks, lane);
+    const long long sr = row_index != nullptr ? row_index[u.r] : u.r;
     const bool ok = sr >= 0 && sr < src_rows;
     if (!ok && lane == 0) set_status(status, MOE_DEVERR_BAD_ROW_TOKEN);
-    if (c < cols)
-      dst[r * cols + c] =
-          from_f32<T>(ok ? static_cast<float>(q[sr * cols + c]) * ckpt_scale(e[sr * nb + b]) : 0.0f);
+    float v[kB];
+    read_blocks(q + sr * cols, e + sr * nb, ok, u.c0, cols, u.b0, nb, lane, v);
+#pragma unroll
+    for (int j = 0; j < kB; ++j)
+      if (u.c0 + 32 * j < cols) dst[u.r * cols + u.c0 + 32 * j] = from_f32<T>(v[j]);
   }
 }
 
@@ -152,73 +200,92 @@ __global__ void __launch_bounds__(256) act_save_kernel(const TS* __restrict__ h,
                                                        int I, int nb, TD* __restrict__ a, int8_t* __restrict__ q,
                                                        uint8_t* __restrict__ e) {
   constexpr int H = SWIGLU ? 2 : 1;
-  const int lane = threadIdx.x & 31;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * nb;
+  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
+  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
   const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
        i += step) {
-    const long long r = i / nb;
-    const int b = static_cast<int>(i - r * nb);
-    const int c = b * kBlk + lane;
-    float v[H];
+    const Piece u = piece(i, chunks, lane);
+    float v[H][kB];
 #pragma unroll
-    for (int j = 0; j < H; ++j) {
-      v[j] = c < I ? to_f32(h[(r * H + j) * I + c]) : 0.0f;
-      const uint32_t ex = __reduce_max_sync(0xffffffffu, abs_bits(v[j])) >> 23;
-      if (c < I) q[(r * H + j) * I + c] = static_cast<int8_t>(ckpt_q(v[j], ckpt_inv_scale(ex)));
-      if (lane == 0) e[(r * H + j) * nb + b] = static_cast<uint8_t>(ex);
-    }
-    if (c < I) {
-      float o, unused;
-      if constexpr (SWIGLU) un2(swiglu(f2(v[0]), f2(v[1])), o, unused);
-      else un2(gelu_sig(f2(v[0])), o, unused);
-      a[r * I + c] = from_f32<TD>(o);
+    for (int m = 0; m < H; ++m) load_blocks(h + (u.r * H + m) * I, u.c0, I, v[m]);
+#pragma unroll
+    for (int m = 0; m < H; ++m)
+      keep_blocks(v[m], u.c0, I, u.b0, nb, lane, q + (u.r * H + m) * I, e + (u.r * H + m) * nb);
+#pragma unroll
+    for (int j = 0; j < kB; j += 2) {
+      float o[2];
+      const F2 h0 = f2(v[0][j], v[0][j + 1]);
+      if constexpr (SWIGLU) un2(swiglu(h0, f2(v[H - 1][j], v[H - 1][j + 1])), o[0], o[1]);
+      else un2(gelu_sig(h0), o[0], o[1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (u.c0 + 32 * (j + t) < I) a[u.r * I + u.c0 + 32 * (j + t)] = from_f32<TD>(o[t]);
     }
   }
 }
 
-// Block per row, so that the row's dot product <da, a> stays inside a block.
+// A row's pieces are spread over `wpr` warps of a block (1, or all 8 where
+// rows are few), so that its dot product <da, a> needs one block at most.
 template <typename TS, typename TD, bool SWIGLU>
 __global__ void __launch_bounds__(256) act_backward_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ e,
                                                            const TS* __restrict__ da, const float* __restrict__ row_w,
-                                                           const int32_t* n_rows, int rows, int I, int nb,
+                                                           const int32_t* n_rows, int rows, int I, int nb, int wpr,
                                                            TD* __restrict__ dh, TD* __restrict__ wa,
                                                            float* __restrict__ dw) {
   constexpr int H = SWIGLU ? 2 : 1;
   __shared__ float s_part[8];
-  const int n = live_rows(n_rows, rows);
-  for (long long r = blockIdx.x; r < n; r += gridDim.x) {
-    const float w = row_w != nullptr ? row_w[r] : 1.0f;
-    float dot = 0.0f;
-    for (int c = threadIdx.x; c < I; c += blockDim.x) {
-      const float g = to_f32(da[r * I + c]);
-      float v[H], a, d[H];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunks = (nb + kB - 1) / kB;
+  const int n = live_rows(n_rows, rows), per = 8 / wpr, part = warp % wpr;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * per; r0 < n; r0 += static_cast<long long>(gridDim.x) * per) {
+    const long long r = r0 + warp / wpr;
+    const bool live = r < n;
+    const F2 w = f2(live && row_w != nullptr ? row_w[r] : 1.0f);
+    F2 dot2 = f2(0.0f);
+    for (int ch = part; live && ch < chunks; ch += wpr) {
+      const int b0 = ch * kB, c0 = b0 * kBlk + lane;
+      float g[kB], v[H][kB];
+      load_blocks(da + r * I, c0, I, g);
 #pragma unroll
-      for (int j = 0; j < H; ++j)
-        v[j] = static_cast<float>(q[(r * H + j) * I + c]) * ckpt_scale(e[(r * H + j) * nb + c / kBlk]);
-      F2 a2, d2[2];
-      float unused;
-      if constexpr (SWIGLU) swiglu_grad(f2(v[0]), f2(v[1]), a2, d2[0], d2[1]);
-      else gelu_sig_grad(f2(v[0]), a2, d2[0]);
-      un2(a2, a, unused);
+      for (int m = 0; m < H; ++m)
+        read_blocks(q + (r * H + m) * I, e + (r * H + m) * nb, true, c0, I, b0, nb, lane, v[m]);
 #pragma unroll
-      for (int j = 0; j < H; ++j) un2(d2[j], d[j], unused);
+      for (int j = 0; j < kB; j += 2) {
+        const F2 h0 = f2(v[0][j], v[0][j + 1]), gj = f2(g[j], g[j + 1]);
+        F2 a, d[2];
+        if constexpr (SWIGLU) swiglu_grad(h0, f2(v[H - 1][j], v[H - 1][j + 1]), a, d[0], d[1]);
+        else gelu_sig_grad(h0, a, d[0]);
+        dot2 = fma2(gj, a, dot2);
+        const F2 wg = w * gj;
+        float o[2], x[H][2];
+        un2(w * a, o[0], o[1]);
 #pragma unroll
-      for (int j = 0; j < H; ++j) dh[(r * H + j) * I + c] = from_f32<TD>(w * g * d[j]);
-      if (wa != nullptr) wa[r * I + c] = from_f32<TD>(w * a);
-      dot = fmaf(g, a, dot);
+        for (int m = 0; m < H; ++m) un2(d[m] * wg, x[m][0], x[m][1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int c = c0 + 32 * (j + t);
+          if (c < I) {
+#pragma unroll
+            for (int m = 0; m < H; ++m) dh[(r * H + m) * I + c] = from_f32<TD>(x[m][t]);
+            if (wa != nullptr) wa[r * I + c] = from_f32<TD>(o[t]);
+          }
+        }
+      }
     }
     if (dw != nullptr) {
+      float dot, dot1;
+      un2(dot2, dot, dot1);
+      dot += dot1;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float t = 0.0f;
-        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) t += s_part[i];
-        dw[r] = t;
+      if (wpr > 1) {
+        if (lane == 0) s_part[warp] = dot;
+        __syncthreads();
+        dot = 0.0f;
+        for (int i = 0; i < wpr; ++i) dot += s_part[warp - part + i];
+        __syncthreads();
       }
-      __syncthreads();
+      if (live && part == 0 && lane == 0) dw[r] = dot;
     }
   }
 }
@@ -544,16 +611,18 @@ inline bool vec_ok(int cols, const void* a, const void* b, const void* c, const 
   return cols % 8 == 0 && any % 16 == 0;
 }
 
-inline int warp_grid(long long units) {
-  return static_cast<int>(std::max<long long>(1, std::min<long long>((units + 7) / 8, 8ll * num_sms())));
-}
 inline int blocks_of(int cols) { return (cols + kBlk - 1) / kBlk; }
+// A warp per piece of kB blocks of a row.
+inline int warp_grid(int rows, int nb) {
+  const long long units = static_cast<long long>(rows) * ((nb + kB - 1) / kB);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>((units + 7) / 8, 32ll * num_sms())));
+}
 
 }  // namespace
 
 cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,
                                  uint8_t* e, cudaStream_t s) {
-  const int nb = blocks_of(cols), grid = warp_grid(static_cast<long long>(rows) * nb);
+  const int nb = blocks_of(cols), grid = warp_grid(rows, nb);
   if (vec_ok(cols, src, q, nullptr, nullptr)) {
     const Shape p = shape(rows, cols);
     if (dtype == MOE_DTYPE_BF16)
@@ -574,7 +643,7 @@ cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_ro
 cudaError_t launch_ckpt_dequantize(int dtype, const int8_t* q, const uint8_t* e, const int32_t* row_index,
                                    const int32_t* n_rows, int rows, int src_rows, int cols, void* dst, int* status,
                                    cudaStream_t s) {
-  const int nb = blocks_of(cols), grid = warp_grid(static_cast<long long>(rows) * nb);
+  const int nb = blocks_of(cols), grid = warp_grid(rows, nb);
   if (vec_ok(cols, dst, q, nullptr, nullptr)) {
     const Shape p = shape(rows, cols);
     if (dtype == MOE_DTYPE_BF16)
@@ -605,7 +674,7 @@ void run_save(const void* h, const int32_t* n_rows, int rows, int I, void* a, in
     const Shape p = shape(rows, I);
     act_save_vec_kernel<TS, TD, SW><<<p.grid, 256, 0, s>>>(hp, n_rows, rows, I, nb, p.lx, ap, q, e);
   } else {
-    act_save_kernel<TS, TD, SW><<<warp_grid(static_cast<long long>(rows) * nb), 256, 0, s>>>(hp, n_rows, rows, I, nb,
+    act_save_kernel<TS, TD, SW><<<warp_grid(rows, nb), 256, 0, s>>>(hp, n_rows, rows, I, nb,
                                                                                              ap, q, e);
   }
 }
@@ -627,8 +696,10 @@ void run_backward(const int8_t* q, const uint8_t* e, const void* da, const float
     const Shape p = shape(rows, I);
     act_backward_vec_kernel<TS, TD, SW><<<p.grid, 256, 0, s>>>(q, e, dp, row_w, n_rows, rows, I, nb, p.lx, hp, wp, dw);
   } else {
-    act_backward_kernel<TS, TD, SW><<<std::min(rows, 8 * num_sms()), 256, 0, s>>>(q, e, dp, row_w, n_rows, rows, I, nb,
-                                                                                  hp, wp, dw);
+    // one warp a row where that fills the GPU, else a block
+    const int wpr = rows >= 6 * 8 * num_sms() ? 1 : 8, per = 8 / wpr;
+    act_backward_kernel<TS, TD, SW><<<std::min((rows - 1) / per + 1, 32 * num_sms()), 256, 0, s>>>(
+        q, e, dp, row_w, n_rows, rows, I, nb, wpr, hp, wp, dw);
   }
 }
 template <typename TS, typename TD>

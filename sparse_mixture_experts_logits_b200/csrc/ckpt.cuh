@@ -16,9 +16,6 @@ __device__ __forceinline__ float ckpt_inv_scale(uint32_t e) {
 __device__ __forceinline__ float ckpt_scale(uint32_t e) {
   return __uint_as_float(e >= 255u ? 0x7fc00000u : (e >= 7u ? (e - 6u) << 23 : 1u << (16u + e)));
 }
-__device__ __forceinline__ int ckpt_q(float v, float inv) {
-  return max(-127, min(127, __float2int_rn(v * inv * 64.0f)));
-}
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 }  // namespace moe

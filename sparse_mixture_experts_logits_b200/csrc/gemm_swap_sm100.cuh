@@ -782,10 +782,10 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         if constexpr (kWgrad) {
           // What a tile of few rows is added onto comes into L2 during its
           // MMAs, instead of when the reducing stores ask for it at the end
-          // (48 experts x 2048 x 5120, 256 rows each: 0.89 -> 0.73 ms; the
+          // (48 experts x 2048 x 5120, 256 rows each: 0.82 -> 0.66 ms; the
           // bytes alone are 0.62).  With more rows to a tile the operand
           // loads behind the prefetches cost more than they gain (512 rows:
-          // 0.94 -> 0.96 ms).
+          // 0.86 -> 0.92 ms).
           if (args.accumulate && t.nkb <= kSwPrefetchKb && col - lane < args.out_cols) {
             const float* line = static_cast<const float*>(args.out) + gofs + row0 * args.ldo + (col - lane);
 #pragma unroll 1
