@@ -26,32 +26,6 @@ __device__ __forceinline__ int live_rows(const int32_t* n_rows, int rows) {
   return n_rows != nullptr ? max(0, min(rows, *n_rows)) : rows;
 }
 
-// Two fp32 values in one register pair: one instruction for both (the
-// activations are otherwise bound by instruction issue beside the memory).
-struct F2 { unsigned long long v; };
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
-__device__ __forceinline__ void un2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 // s = sigmoid(x) and d = s (1 - s) from y = x log2(e), without a difference:
 // with z = exp(-x) they are s = 1 / (1 + z) and (z s) s.  The hardware's
 // exponential (2 ulp) and reciprocal (1 ulp, 0 instead of a subnormal); the

@@ -154,8 +154,12 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
                       L.layout == kSwWgradRagged ? 128 : 32, L.layout == kSwWgradRagged ? kSwRgBufRows : 32))
       return cudaErrorInvalidValue;
   } else {
+    // a box is used by tiles wider than twice the next smaller one (few rows: the small boxes alone)
+    const long long widest = std::min<long long>(kSwMaxTile, (L.rows + 15) / 16 * 16);
     for (int i = 0; i < kSwBoxes; ++i)
-      if (!tmap_bf16(&m.x[i], L.X, L.x_rows, L.K, swap_box_rows(i))) return cudaErrorInvalidValue;
+      if ((i + 1 == kSwBoxes || 2 * swap_box_rows(i + 1) < widest) &&
+          !tmap_bf16(&m.x[i], L.X, L.x_rows, L.K, swap_box_rows(i)))
+        return cudaErrorInvalidValue;
   }
   SwapArgs a = {};
   a.num_groups = L.num_groups;

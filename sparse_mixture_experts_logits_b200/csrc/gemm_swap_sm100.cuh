@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       }
       fence_mbar_init();
       tma_prefetch_desc(&maps.w);
-      tma_prefetch_desc(&maps.x[0]);
+      tma_prefetch_desc(&maps.x[kBMn ? 0 : kSwBoxes - 1]);
       if constexpr (kWgrad) tma_prefetch_desc(&maps.out);
     }
   } else if (warp == 1) {

@@ -5,10 +5,12 @@
 //   forward   y[r, n]   = sum_k x[r, k]  W_g[n, k] (+ b_g[n])
 //   dgrad     dx[r, k]  = sum_n dy[r, n] W_g[n, k]
 //   wgrad     dW_g[n,k] = sum_r dy[r, n] x[r, k]     over g's rows
-// 64 x 64 output tiles, 16-deep slices through shared memory, a 4 x 4 block
-// of sums per thread.  Every 128 terms the block's partial sums are added to
-// its totals, so that a sum of thousands of terms does not lose the small
-// ones; all orders are fixed.
+// 64 x 64 output tiles, 16-deep slices through shared memory (fp32: four
+// stages of 4-byte asynchronous copies, which suit any width and alignment;
+// bf16: the next slice through registers), a 4 x 4 block of neighbouring sums per
+// thread: two 16-byte shared loads feed 16 multiply-adds.  Every 128 terms the block's partial sums are added to its
+// totals, so that a sum of thousands of terms does not lose the small ones;
+// all orders are fixed.
 #include <algorithm>
 
 #include "grouped_colsum.cuh"
@@ -19,6 +21,16 @@ namespace {
 
 constexpr int kTM = 64, kTN = 64, kTK = 16, kThreads = 256;
 constexpr int kChunkSlices = 8;
+constexpr int kStages = 4;
+
+// 4 bytes global -> shared, or zeros (nothing is read then).
+__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 struct Args {
   const void* A; long long a_sm, a_sc;             // A(m, c) = A[m a_sm + c a_sc]
@@ -36,9 +48,10 @@ struct Args {
 };
 
 template <typename T, typename TO, bool WGRAD>
-__global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
-  __shared__ float As[kTK][kTM + 1];
-  __shared__ float Bs[kTK][kTN + 1];
+__global__ void __launch_bounds__(kThreads, 2) grouped_simt_kernel(const Args p) {
+  constexpr bool kAsync = sizeof(T) == 4;
+  __shared__ __align__(16) float As[kStages][kTK][kTM + 4];
+  __shared__ __align__(16) float Bs[kStages][kTK][kTN + 4];
   __shared__ int s_off[kMaxExperts + 1];
   __shared__ int s_tstart[kMaxExperts + 1];
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -85,38 +98,82 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
     const long long bg = static_cast<long long>(g) * p.b_gstride;
     float acc[4][4] = {}, tot[4][4] = {};
     int slices = 0;
-    // this thread's elements of a slice, along each operand's contiguous
-    // index; the next slice is loaded while this one is multiplied
+    // This thread's elements of a slice, along each operand's contiguous
+    // index: four of A and four of B.  Their addresses in the first slice, and for each how many
+    // contraction steps are left from there (0: a row or column behind the tile).
     constexpr int kPer = kTM * kTK / kThreads;
-    float ra[kPer], rb[kPer];
-    auto fetch = [&](long long k0) {
+    const int tid = threadIdx.x;
+    const T *pa[kPer], *pb[kPer];
+    int left_a[kPer], left_b[kPer];
+    int ma[kPer], ca[kPer], nb[kPer], db[kPer];
+    const int len = static_cast<int>(c1 - c0);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        int m, c, n, d;
-        if (p.a_sc == 1) { c = i & (kTK - 1); m = i / kTK; } else { m = i & (kTM - 1); c = i / kTM; }
-        if (p.b_sc == 1) { d = i & (kTK - 1); n = i / kTK; } else { n = i & (kTN - 1); d = i / kTN; }
-        ra[j] = (m < nm && k0 + c < c1) ? to_f32(A[(m0 + m) * p.a_sm + (k0 + c) * p.a_sc]) : 0.f;
-        rb[j] = (n0 + n < p.N && k0 + d < c1) ? to_f32(B[bg + (n0 + n) * p.b_sn + (k0 + d) * p.b_sc]) : 0.f;
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * kThreads;
+      if (p.a_sc == 1) { ca[j] = i & (kTK - 1); ma[j] = i / kTK; } else { ma[j] = i & (kTM - 1); ca[j] = i / kTM; }
+      if (p.b_sc == 1) { db[j] = i & (kTK - 1); nb[j] = i / kTK; } else { nb[j] = i & (kTN - 1); db[j] = i / kTN; }
+      left_a[j] = ma[j] < nm ? len - ca[j] : 0;
+      left_b[j] = n0 + nb[j] < p.N ? len - db[j] : 0;
+      pa[j] = left_a[j] > 0 ? A + (m0 + ma[j]) * p.a_sm + (c0 + ca[j]) * p.a_sc : A;
+      pb[j] = left_b[j] > 0 ? B + bg + (n0 + nb[j]) * p.b_sn + (c0 + db[j]) * p.b_sc : B;
+    }
+    const long long step_a = kTK * p.a_sc, step_b = kTK * p.b_sc;
+    int at_k = 0;  // contraction steps of the slices asked for so far
+    float ra[kPer], rb[kPer];
+    auto copy = [&](int to) {  // fp32: the next slice into stage `to`, asynchronously
+      if constexpr (kAsync) {
+        if (at_k < len) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const bool oka = at_k < left_a[j], okb = at_k < left_b[j];
+            copy4_async(&As[to][ca[j]][ma[j]], oka ? pa[j] : A, oka);
+            copy4_async(&Bs[to][db[j]][nb[j]], okb ? pb[j] : B, okb);
+            pa[j] += step_a;
+            pb[j] += step_b;
+          }
+        }
+        at_k += kTK;
+        copies_commit();  // an empty group behind the end keeps the count
       }
     };
-    fetch(c0);
-    for (long long k0 = c0; k0 < c1; k0 += kTK) {
+    auto fetch = [&]() {  // bf16: the next slice into registers
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        if (p.a_sc == 1) As[i & (kTK - 1)][i / kTK] = ra[j]; else As[i / kTM][i & (kTM - 1)] = ra[j];
-        if (p.b_sc == 1) Bs[i & (kTK - 1)][i / kTK] = rb[j]; else Bs[i / kTN][i & (kTN - 1)] = rb[j];
+        ra[j] = at_k < left_a[j] ? to_f32(*pa[j]) : 0.f;
+        rb[j] = at_k < left_b[j] ? to_f32(*pb[j]) : 0.f;
+        pa[j] += step_a;
+        pb[j] += step_b;
       }
-      __syncthreads();
-      if (k0 + kTK < c1) fetch(k0 + kTK);
+      at_k += kTK;
+    };
+    auto put = [&](int to) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        As[to][ca[j]][ma[j]] = ra[j];
+        Bs[to][db[j]][nb[j]] = rb[j];
+      }
+    };
+    int st = 0;
+    if constexpr (kAsync) {
+      for (int i = 0; i < kStages - 1; ++i) copy(i);
+    } else if (len > 0) {
+      fetch();
+    }
+    for (int k0 = 0; k0 < len; k0 += kTK, st = (st + 1) & (kStages - 1)) {
+      if constexpr (kAsync) {
+        copies_wait<kStages - 2>();  // this slice has arrived (for this thread)
+        __syncthreads();             // for every thread, and the stage before is read
+        copy((st + kStages - 1) & (kStages - 1));
+      } else {
+        put(st);
+        __syncthreads();
+        if (k0 + kTK < len) fetch();
+      }
 #pragma unroll
       for (int kk = 0; kk < kTK; ++kk) {
-        float a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = As[kk][ty + 16 * i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = Bs[kk][tx + 16 * j];
+        const float4 a4 = *reinterpret_cast<const float4*>(&As[st][kk][4 * ty]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&Bs[st][kk][4 * tx]);
+        const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -129,16 +186,17 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const Args p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) { tot[i][j] += acc[i][j]; acc[i][j] = 0.f; }
       }
-      __syncthreads();
     }
+    if constexpr (kAsync) copies_wait<0>();
+    __syncthreads();  // the tile's stages are read before the next tile fills them
     const long long cg = WGRAD ? static_cast<long long>(g) * p.c_gstride : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int m = ty + 16 * i;
+      const int m = 4 * ty + i;
       if (m >= nm) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
+        const int n = n0 + 4 * tx + j;
         if (n >= p.N) continue;
         float v = tot[i][j] + acc[i][j];
         if (p.bias != nullptr) v += to_f32(static_cast<const T*>(p.bias)[static_cast<long long>(g) * p.N + n]);

@@ -70,7 +70,7 @@ class _Handle:
         return stream.cuda_stream
 
     def _call(self, fn, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if torch._C._cuda_getDevice() == self.device.index:
             fn(*args)
         else:
             with torch.cuda.device(self.device):
