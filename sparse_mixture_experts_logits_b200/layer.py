@@ -127,7 +127,7 @@ class MoELayer:
             if self._save is None:
                 nbytes = abi.moe_forward_save_workspace_size(self.desc)
                 # a bf16 layer keeps them from its own workspace
-                self._save = (self.ws_ptr, self.ws_bytes, None) if nbytes <= self.ws_bytes else self._scratch(nbytes)
+                self._save = (self.ws_ptr, self.ws_bytes, None) if nbytes <= self.ws_bytes else self._scratch(nbytes, stream)
             abi.moe_forward_save(self.desc, self.weights, x.data_ptr(), _ptr(addend), y.data_ptr(), checkpoint.ptr,
                                  checkpoint.nbytes, self._save[0], self._save[1], _stream_handle(stream))
             return y
@@ -139,9 +139,10 @@ class MoELayer:
                                 self.ws_ptr, self.ws_bytes, _stream_handle(stream))
         return y
 
-    def _scratch(self, nbytes: int):
-        """(256-byte aligned address, bytes, buffer)"""
-        buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
+    def _scratch(self, nbytes: int, stream):
+        """(256-byte aligned address, bytes, buffer), allocated on the stream that will use it"""
+        with torch.cuda.stream(stream):
+            buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
         return buf.data_ptr() + (-buf.data_ptr()) % 256, nbytes, buf
 
     def device_status(self, stream=None) -> int:
@@ -167,7 +168,7 @@ class MoELayer:
         routing it recomputed.  With the ``checkpoint`` of a forward on the
         same x nothing of that forward is recomputed (moe_backward_saved)."""
         if checkpoint is not None and self._cws is None:
-            self._cws = self._scratch(abi.moe_backward_saved_workspace_size(self.desc))
+            self._cws = self._scratch(abi.moe_backward_saved_workspace_size(self.desc), stream)
         if checkpoint is None and self._bws is None:
             self.bws_bytes = abi.moe_backward_workspace_size(self.desc)
             if self.bws_bytes == 0:

@@ -5,10 +5,12 @@ holds its workspace or checkpoint and calls the C ABI; no computation happens
 here, and nothing is recorded for autograd.
 
 Every call runs on ``stream``, or on the current stream of the handle's device
-when none is given (the caller keeps tensors made on another stream alive and
-ordered, as for any torch extension).  Calls of one handle share its workspace
-or checkpoint, so they must be ordered on one stream; a step that is captured
-into a CUDA graph and replayed beside eager calls takes a handle of its own.
+when none is given; what it allocates (outputs, and at the first call the
+workspace) is allocated on that stream.  The caller keeps tensors made on
+another stream alive and ordered, as for any torch extension.  Calls of one
+handle share its workspace or checkpoint, so they must be ordered on one
+stream; a step that is captured into a CUDA graph and replayed beside eager
+calls takes a handle of its own.
 """
 from __future__ import annotations
 
@@ -50,17 +52,23 @@ class _Handle:
     def _opt(self, name, t, shape, dtype):
         return None if t is None else self._in(name, t, shape, dtype)
 
-    def _out(self, name, t, shape, dtype):
-        if t is None:
+    def _new(self, shape, dtype, stream):
+        if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _out(self, name, t, shape, dtype, stream=None):
+        if t is None:
+            return self._new(shape, dtype, stream)
         self._in(name, t, shape, dtype)
         return t
 
-    def _wanted(self, name, t, shape, dtype):
+    def _wanted(self, name, t, shape, dtype, stream):
         """An optional output: False or None (not written), True (allocated) or a tensor."""
         if t is None or t is False:
             return None
-        return self._out(name, None if t is True else t, shape, dtype)
+        return self._out(name, None if t is True else t, shape, dtype, stream)
 
     def _stream(self, stream):
         if stream is None:
@@ -76,10 +84,10 @@ class _Handle:
             with torch.cuda.device(self.device):
                 fn(*args)
 
-    def _workspace(self, nbytes):
-        """(buffer, 256-byte aligned address)"""
-        buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
-        return buf, buf.data_ptr() + (-buf.data_ptr()) % 256
+    def _workspace(self, nbytes, stream):
+        """(256-byte aligned address, bytes, buffer); every call clears the status word itself"""
+        buf = self._new((nbytes + 256,), torch.uint8, stream)
+        return buf.data_ptr() + (-buf.data_ptr()) % 256, nbytes, buf
 
 
 class GroupedLinear(_Handle):
@@ -111,18 +119,19 @@ class GroupedLinear(_Handle):
         self._ws_bytes = abi.moe_grouped_workspace_size(*self._dims)
         if self._ws_bytes == 0:
             raise abi.MoEError("moe_grouped_workspace_size", abi.MOE_ERR_INVALID_ARG)
-        self._ws, self._ws_ptr = self._workspace(self._ws_bytes)
-        self._wg = None
+        self._ws = self._wg = None  # the row products' workspace, the weight gradient's
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
         """y[r] = x[r] W_g^T (+ bias[g])."""
         px = self._in("x", x, (self.rows, self.K), self.dtype)
         po = self._in("offsets", offsets, (self.G + 1,), torch.int32)
-        y = self._out("y", y, (self.rows, self.N), self.out_dtype)
+        y = self._out("y", y, (self.rows, self.N), self.out_dtype, stream)
+        if self._ws is None:
+            self._ws = self._workspace(self._ws_bytes, stream)
         self._call(abi.moe_grouped_gemm, px, self.weight.data_ptr(),
                    None if self.bias is None else self.bias.data_ptr(), po, *self._dims, self._odt, y.data_ptr(),
-                   self._ws_ptr, self._ws_bytes, self._stream(stream))
+                   self._ws[0], self._ws_bytes, self._stream(stream))
         return y
 
     def input_grad(self, dy: torch.Tensor, offsets: torch.Tensor, dx: torch.Tensor | None = None,
@@ -130,9 +139,11 @@ class GroupedLinear(_Handle):
         """dx[r] = dy[r] W_g."""
         pd = self._in("dy", dy, (self.rows, self.N), self.dtype)
         po = self._in("offsets", offsets, (self.G + 1,), torch.int32)
-        dx = self._out("dx", dx, (self.rows, self.K), self.out_dtype)
+        dx = self._out("dx", dx, (self.rows, self.K), self.out_dtype, stream)
+        if self._ws is None:
+            self._ws = self._workspace(self._ws_bytes, stream)
         self._call(abi.moe_grouped_dgrad, pd, self.weight.data_ptr(), po, *self._dims, self._odt, dx.data_ptr(),
-                   self._ws_ptr, self._ws_bytes, self._stream(stream))
+                   self._ws[0], self._ws_bytes, self._stream(stream))
         return dx
 
     def weight_grad(self, x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, dw: torch.Tensor | None = None,
@@ -145,21 +156,20 @@ class GroupedLinear(_Handle):
         px = self._in("x", x, (self.rows, self.K), self.dtype)
         pd = self._in("dy", dy, (self.rows, self.N), self.dtype)
         po = self._in("offsets", offsets, (self.G + 1,), torch.int32)
-        dw = self._out("dw", dw, (self.G, self.N, self.K), torch.float32)
-        db = self._wanted("db", db, (self.G, self.N), torch.float32)
+        dw = self._out("dw", dw, (self.G, self.N, self.K), torch.float32, stream)
+        db = self._wanted("db", db, (self.G, self.N), torch.float32, stream)
         if self._wg is None:
-            nbytes = abi.moe_grouped_wgrad_workspace_size(*self._dims)
-            self._wg = (*self._workspace(nbytes), nbytes)
+            self._wg = self._workspace(abi.moe_grouped_wgrad_workspace_size(*self._dims), stream)
         self._call(abi.moe_grouped_wgrad, px, pd, po, *self._dims, int(bool(accumulate)), dw.data_ptr(),
-                   None if db is None else db.data_ptr(), self._wg[1], self._wg[2], self._stream(stream))
+                   None if db is None else db.data_ptr(), self._wg[0], self._wg[1], self._stream(stream))
         return dw, db
 
     def device_status(self, stream=None) -> int:
         """The first error that the last calls' kernels reported (0: none), and clears it.  Synchronises."""
         s = self._stream(stream)
         with torch.cuda.device(self.device):
-            code = abi.moe_device_status(self._ws_ptr, s)
-            return code if code or self._wg is None else abi.moe_device_status(self._wg[1], s)
+            codes = [abi.moe_device_status(ws[0], s) for ws in (self._ws, self._wg) if ws is not None]
+        return next((c for c in codes if c), 0)
 
 
 class RowCheckpoint(_Handle):
@@ -188,7 +198,7 @@ class RowCheckpoint(_Handle):
         range gives a zero row and sets ``status``)."""
         n = self.rows if row_index is None else row_index.numel()
         pi = self._opt("row_index", row_index, (n,), torch.int32)
-        out = self._out("out", out, (n, self.cols), self.dtype)
+        out = self._out("out", out, (n, self.cols), self.dtype, stream)
         self._call(abi.moe_ckpt_dequantize, self.q.data_ptr(), self.e.data_ptr(), pi,
                    self._opt("n_rows", n_rows, (1,), torch.int32), n, self.rows, self.cols, self._dt, out.data_ptr(),
                    self.status.data_ptr(), self._stream(stream))
@@ -224,14 +234,14 @@ class ActivationCheckpoint(_Handle):
              stream=None) -> torch.Tensor:
         """a = act(h); h is kept."""
         ph = self._in("h", h, (self.rows, self.width), self.src_dtype)
-        a = self._out("a", a, (self.rows, self.I), self.dtype)
+        a = self._out("a", a, (self.rows, self.I), self.dtype, stream)
         self._call(abi.moe_act_save, ph, self._opt("n_rows", n_rows, (1,), torch.int32), self.rows, self.I, *self._dts,
                    a.data_ptr(), self.q.data_ptr(), self.e.data_ptr(), self._stream(stream))
         return a
 
     def load(self, stream=None) -> torch.Tensor:
         """The kept h [rows, width], in dtype."""
-        out = torch.empty((self.rows, self.width), dtype=self.dtype, device=self.device)
+        out = self._new((self.rows, self.width), self.dtype, stream)
         n = self.rows * self._halves
         self._call(abi.moe_ckpt_dequantize, self.q.data_ptr(), self.e.data_ptr(), None, None, n, n, self.I,
                    self._dts[1], out.data_ptr(), None, self._stream(stream))
@@ -246,9 +256,9 @@ class ActivationCheckpoint(_Handle):
         h.  wa and dw are written when True or a tensor is given."""
         pd = self._in("da", da, (self.rows, self.I), self.src_dtype)
         pw = self._opt("row_w", row_w, (self.rows,), torch.float32)
-        dh = self._out("dh", dh, (self.rows, self.width), self.dtype)
-        wa = self._wanted("wa", wa, (self.rows, self.I), self.dtype)
-        dw = self._wanted("dw", dw, (self.rows,), torch.float32)
+        dh = self._out("dh", dh, (self.rows, self.width), self.dtype, stream)
+        wa = self._wanted("wa", wa, (self.rows, self.I), self.dtype, stream)
+        dw = self._wanted("dw", dw, (self.rows,), torch.float32, stream)
         self._call(abi.moe_act_backward, self.q.data_ptr(), self.e.data_ptr(), pd, pw,
                    self._opt("n_rows", n_rows, (1,), torch.int32), self.rows, self.I, *self._dts, dh.data_ptr(),
                    None if wa is None else wa.data_ptr(), None if dw is None else dw.data_ptr(),

@@ -259,6 +259,34 @@ def test_checkpoints_off_their_boundaries(moe, act):
     assert torch.equal(c1.q, c2.q) and torch.equal(c1.load(), c2.load(out=off(h)))
 
 
+def test_a_stream_of_its_own(moe):
+    """Calls on a given stream while the current one is busy: nothing they allocate waits for, or is written by, the
+    current stream."""
+    counts = [40, 0, 7, 100]
+    offsets, N, K = _offsets(counts), 48, 88
+    rows = int(offsets[-1])
+    off, x, w, dy = _dev(offsets), _randn(1, (rows, K), torch.bfloat16), _randn(2, (4, N, K), torch.bfloat16), _randn(3, (rows, N), torch.bfloat16)
+    op = moe.GroupedLinear(w, rows)
+    want = op.forward(x, off), op.input_grad(dy, off), *op.weight_grad(x, dy, off, db=True)
+    ck = moe.ActivationCheckpoint("gelu_tanh", rows, K, torch.bfloat16)
+    kept = ck.save(x), ck.load(), *ck.backward(x, wa=True, dw=True)
+    torch.cuda.synchronize()
+    side, busy = torch.cuda.Stream(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        junk = [torch.full((rows, N), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+        for _ in range(40):
+            busy.fill_(1)
+        del junk
+        op = moe.GroupedLinear(w, rows)
+        ck = moe.ActivationCheckpoint("gelu_tanh", rows, K, torch.bfloat16)
+        got = op.forward(x, off, stream=side), op.input_grad(dy, off, stream=side), *op.weight_grad(x, dy, off, db=True, stream=side)
+        again = ck.save(x, stream=side), ck.load(stream=side), *ck.backward(x, wa=True, dw=True, stream=side)
+        torch.cuda.synchronize()
+        for g, v in zip(got + again, want + kept):
+            assert torch.equal(g, v)
+        assert op.device_status(stream=side) == 0
+
+
 def test_no_rows(moe):
     w = _randn(1, (3, 16, 24), torch.bfloat16)
     op = moe.GroupedLinear(w, 0)
