@@ -88,66 +88,100 @@ __device__ __forceinline__ void swiglu_grad(F2 g, F2 u, F2& a, F2& dg, F2& du) {
 // A warp takes kB blocks of 32 columns of a row at a time, a lane one column
 // of each: every access is a value wide, so that nothing is asked of the
 // width or the alignment, and kB (times the halves) loads are in flight.
+// FULL: all of the kB blocks lie inside the row, and nothing is compared.
 constexpr int kB = 8;
 
-// The kB values of this lane at columns c0 + 32 j (0 behind the row).
-template <typename T>
-__device__ __forceinline__ void load_blocks(const T* __restrict__ row, int c0, int cols, float (&v)[kB]) {
+// This lane's kB values, from its first column on (`left`: columns from there
+// to the row's end; 0 behind it).
+template <bool FULL, typename T>
+__device__ __forceinline__ void load_blocks(const T* __restrict__ p, int left, float (&v)[kB]) {
 #pragma unroll
-  for (int j = 0; j < kB; ++j) {
-    const int c = c0 + 32 * j;
-    v[j] = c < cols ? to_f32(row[c]) : 0.0f;
-  }
+  for (int j = 0; j < kB; ++j) v[j] = FULL || 32 * j < left ? to_f32(p[32 * j]) : 0.0f;
 }
-// Keeps them: q of the row and, lane j, the exponent of block b0 + j.
-__device__ __forceinline__ void keep_blocks(const float (&v)[kB], int c0, int cols, int b0, int nb, int lane,
-                                            int8_t* __restrict__ q, uint8_t* __restrict__ e) {
-  uint32_t mine = 0;
-#pragma unroll
-  for (int j = 0; j < kB; ++j) {
-    const uint32_t ex = __reduce_max_sync(0xffffffffu, abs_bits(v[j])) >> 23;
-    if (lane == j) mine = ex;
-    const float t = fminf(fmaxf(v[j] * ckpt_inv_scale(ex), -127.0f / 64.0f), 127.0f / 64.0f);
-    const uint32_t bits = ex == 255u ? 0u : __float_as_uint(fmaf(t, 64.0f, 12582912.0f));  // see keep8
-    const int c = c0 + 32 * j;
-    if (c < cols) q[c] = static_cast<int8_t>(bits);
-  }
-  if (lane < kB && b0 + lane < nb) e[b0 + lane] = static_cast<uint8_t>(mine);
-}
-// The kept values of those columns.
-__device__ __forceinline__ void read_blocks(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, bool ok, int c0,
-                                            int cols, int b0, int nb, int lane, float (&v)[kB]) {
-  int k[kB];
-#pragma unroll
-  for (int j = 0; j < kB; ++j) k[j] = ok && c0 + 32 * j < cols ? q[c0 + 32 * j] : 0;
-  const float s = ckpt_scale(ok && lane < kB && b0 + lane < nb ? e[b0 + lane] : 0u);
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_blocks(T* __restrict__ p, int left, const float (&v)[kB]) {
 #pragma unroll
   for (int j = 0; j < kB; ++j)
-    v[j] = (__uint_as_float(0x4B000000u + static_cast<uint32_t>(k[j] + 128)) - 8388736.0f) *
-           __shfl_sync(0xffffffffu, s, j);
+    if (FULL || 32 * j < left) p[32 * j] = from_f32<T>(v[j]);
+}
+// Keeps them: q from this lane's first column on and, lane j, the exponent of
+// block j.  Rounded as in keep8, with the same long way for the rare rest.
+template <bool FULL>
+__device__ __forceinline__ void keep_blocks(const float (&v)[kB], int left, int blocks, int lane,
+                                            int8_t* __restrict__ q, uint8_t* __restrict__ e) {
+  uint32_t mine = 0, ex[kB], b[kB];
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < kB; ++j) {
+    ex[j] = __reduce_max_sync(0xffffffffu, abs_bits(v[j])) >> 23;
+    if (lane == j) mine = ex[j];
+    b[j] = __float_as_uint(fmaf(v[j], __uint_as_float((260u - ex[j]) << 23), 12582912.0f));
+    odd |= (b[j] & 0xffu) == 0x80u || ex[j] - 6u > 248u;
+  }
+  if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+      const float t = fminf(fmaxf(v[j] * ckpt_inv_scale(ex[j]), -127.0f / 64.0f), 127.0f / 64.0f);
+      b[j] = ex[j] == 255u ? 0u : __float_as_uint(fmaf(t, 64.0f, 12582912.0f));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kB; ++j)
+    if (FULL || 32 * j < left) q[32 * j] = static_cast<int8_t>(b[j]);
+  if (lane < blocks) e[lane] = static_cast<uint8_t>(mine);
+}
+// The kept values of those columns (0 where `ok` is false).
+template <bool FULL>
+__device__ __forceinline__ void read_blocks(const int8_t* __restrict__ q, const uint8_t* __restrict__ e, bool ok,
+                                            int left, int blocks, int lane, float (&v)[kB]) {
+  int k[kB];
+#pragma unroll
+  for (int j = 0; j < kB; ++j) k[j] = ok && (FULL || 32 * j < left) ? q[32 * j] : 0;
+  const float s = ckpt_scale(ok && lane < blocks ? e[lane] : 0u);
+#pragma unroll
+  for (int j = 0; j < kB; ++j)
+    v[j] = (__uint_as_float(0x4B000080u + static_cast<uint32_t>(k[j])) - 8388736.0f) * __shfl_sync(0xffffffffu, s, j);
 }
 
-// Unit i of a batch: `chunks` pieces of kB blocks a row.
-struct Piece { long long r; int b0, c0; };
-__device__ __forceinline__ Piece piece(long long i, int chunks, int lane) {
-  const long long r = i / chunks;
-  const int b0 = static_cast<int>(i - r * chunks) * kB;
-  return {r, b0, b0 * kBlk + lane};
+// This warp's pieces of a batch: `chunks` of kB blocks a row, every
+// gridDim x 8-th piece, stepped without a division.
+struct Walk {
+  long long r;
+  int ch, dq, dr, chunks;
+  __device__ explicit Walk(int nb) : chunks((nb + kB - 1) / kB) {
+    const int start = blockIdx.x * 8 + (threadIdx.x >> 5), step = gridDim.x * 8;
+    r = start / chunks;
+    ch = start % chunks;
+    dq = step / chunks;
+    dr = step % chunks;
+  }
+  __device__ void next() {
+    r += dq;
+    ch += dr;
+    if (ch >= chunks) { ch -= chunks; ++r; }
+  }
+};
+// Calls f(true) for a piece inside the row and f(false) for the row's end
+// (as types: the branch is the warp's).
+template <bool V> struct Bool { static constexpr bool value = V; };
+template <typename F>
+__device__ __forceinline__ void full_or_not(bool full, F&& f) {
+  if (full) f(Bool<true>()); else f(Bool<false>());
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) ckpt_quantize_kernel(const T* __restrict__ src, const int32_t* n_rows, int rows,
                                                             int cols, int nb, int8_t* __restrict__ q,
                                                             uint8_t* __restrict__ e) {
-  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
-       i += step) {
-    const Piece u = piece(i, chunks, lane);
-    float v[kB];
-    load_blocks(src + u.r * cols, u.c0, cols, v);
-    keep_blocks(v, u.c0, cols, u.b0, nb, lane, q + u.r * cols, e + u.r * nb);
+  const int lane = threadIdx.x & 31, n = live_rows(n_rows, rows);
+  for (Walk w(nb); w.r < n; w.next()) {
+    const int b0 = w.ch * kB, c0 = b0 * kBlk + lane;
+    full_or_not((b0 + kB) * kBlk <= cols, [&](auto full) {
+      constexpr bool F = decltype(full)::value;
+      float v[kB];
+      load_blocks<F>(src + w.r * cols + c0, cols - c0, v);
+      keep_blocks<F>(v, cols - c0, nb - b0 < kB ? nb - b0 : kB, lane, q + w.r * cols + c0, e + w.r * nb + b0);
+    });
   }
 }
 
@@ -157,20 +191,19 @@ __global__ void __launch_bounds__(256) ckpt_dequantize_kernel(const int8_t* __re
                                                               const int32_t* __restrict__ row_index,
                                                               const int32_t* n_rows, int rows, int src_rows, int cols,
                                                               int nb, T* __restrict__ dst, int* status) {
-  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
-       i += step) {
-    const Piece u = piece(i, chunks, lane);
-    const long long sr = row_index != nullptr ? row_index[u.r] : u.r;
+  const int lane = threadIdx.x & 31, n = live_rows(n_rows, rows);
+  for (Walk w(nb); w.r < n; w.next()) {
+    const int b0 = w.ch * kB, c0 = b0 * kBlk + lane;
+    const long long sr = row_index != nullptr ? row_index[w.r] : w.r;
     const bool ok = sr >= 0 && sr < src_rows;
     if (!ok && lane == 0) set_status(status, MOE_DEVERR_BAD_ROW_TOKEN);
-    float v[kB];
-    read_blocks(q + sr * cols, e + sr * nb, ok, u.c0, cols, u.b0, nb, lane, v);
-#pragma unroll
-    for (int j = 0; j < kB; ++j)
-      if (u.c0 + 32 * j < cols) dst[u.r * cols + u.c0 + 32 * j] = from_f32<T>(v[j]);
+    full_or_not((b0 + kB) * kBlk <= cols, [&](auto full) {
+      constexpr bool F = decltype(full)::value;
+      float v[kB];
+      read_blocks<F>(q + (ok ? sr : 0) * cols + c0, e + (ok ? sr : 0) * nb + b0, ok, cols - c0,
+                     nb - b0 < kB ? nb - b0 : kB, lane, v);
+      store_blocks<F>(dst + w.r * cols + c0, cols - c0, v);
+    });
   }
 }
 
@@ -179,28 +212,26 @@ __global__ void __launch_bounds__(256) act_save_kernel(const TS* __restrict__ h,
                                                        int I, int nb, TD* __restrict__ a, int8_t* __restrict__ q,
                                                        uint8_t* __restrict__ e) {
   constexpr int H = SWIGLU ? 2 : 1;
-  const int lane = threadIdx.x & 31, chunks = (nb + kB - 1) / kB;
-  const long long units = static_cast<long long>(live_rows(n_rows, rows)) * chunks;
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < units;
-       i += step) {
-    const Piece u = piece(i, chunks, lane);
-    float v[H][kB];
+  const int lane = threadIdx.x & 31, n = live_rows(n_rows, rows);
+  for (Walk w(nb); w.r < n; w.next()) {
+    const int b0 = w.ch * kB, c0 = b0 * kBlk + lane;
+    full_or_not((b0 + kB) * kBlk <= I, [&](auto full) {
+      constexpr bool F = decltype(full)::value;
+      const int left = I - c0, blocks = nb - b0 < kB ? nb - b0 : kB;
+      float v[H][kB], o[kB];
 #pragma unroll
-    for (int m = 0; m < H; ++m) load_blocks(h + (u.r * H + m) * I, u.c0, I, v[m]);
+      for (int m = 0; m < H; ++m) load_blocks<F>(h + (w.r * H + m) * I + c0, left, v[m]);
 #pragma unroll
-    for (int m = 0; m < H; ++m)
-      keep_blocks(v[m], u.c0, I, u.b0, nb, lane, q + (u.r * H + m) * I, e + (u.r * H + m) * nb);
+      for (int m = 0; m < H; ++m)
+        keep_blocks<F>(v[m], left, blocks, lane, q + (w.r * H + m) * I + c0, e + (w.r * H + m) * nb + b0);
 #pragma unroll
-    for (int j = 0; j < kB; j += 2) {
-      float o[2];
-      const F2 h0 = f2(v[0][j], v[0][j + 1]);
-      if constexpr (SWIGLU) un2(swiglu(h0, f2(v[H - 1][j], v[H - 1][j + 1])), o[0], o[1]);
-      else un2(gelu_sig(h0), o[0], o[1]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (u.c0 + 32 * (j + t) < I) a[u.r * I + u.c0 + 32 * (j + t)] = from_f32<TD>(o[t]);
-    }
+      for (int j = 0; j < kB; j += 2) {
+        const F2 h0 = f2(v[0][j], v[0][j + 1]);
+        if constexpr (SWIGLU) un2(swiglu(h0, f2(v[H - 1][j], v[H - 1][j + 1])), o[j], o[j + 1]);
+        else un2(gelu_sig(h0), o[j], o[j + 1]);
+      }
+      store_blocks<F>(a + w.r * I + c0, left, o);
+    });
   }
 }
 
@@ -223,33 +254,30 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const int8_t* __restr
     F2 dot2 = f2(0.0f);
     for (int ch = part; live && ch < chunks; ch += wpr) {
       const int b0 = ch * kB, c0 = b0 * kBlk + lane;
-      float g[kB], v[H][kB];
-      load_blocks(da + r * I, c0, I, g);
+      full_or_not((b0 + kB) * kBlk <= I, [&](auto full) {
+        constexpr bool F = decltype(full)::value;
+        const int left = I - c0, blocks = nb - b0 < kB ? nb - b0 : kB;
+        float g[kB], v[H][kB], o[kB];
+        load_blocks<F>(da + r * I + c0, left, g);
 #pragma unroll
-      for (int m = 0; m < H; ++m)
-        read_blocks(q + (r * H + m) * I, e + (r * H + m) * nb, true, c0, I, b0, nb, lane, v[m]);
+        for (int m = 0; m < H; ++m)
+          read_blocks<F>(q + (r * H + m) * I + c0, e + (r * H + m) * nb + b0, true, left, blocks, lane, v[m]);
 #pragma unroll
-      for (int j = 0; j < kB; j += 2) {
-        const F2 h0 = f2(v[0][j], v[0][j + 1]), gj = f2(g[j], g[j + 1]);
-        F2 a, d[2];
-        if constexpr (SWIGLU) swiglu_grad(h0, f2(v[H - 1][j], v[H - 1][j + 1]), a, d[0], d[1]);
-        else gelu_sig_grad(h0, a, d[0]);
-        dot2 = fma2(gj, a, dot2);
-        const F2 wg = w * gj;
-        float o[2], x[H][2];
-        un2(w * a, o[0], o[1]);
+        for (int j = 0; j < kB; j += 2) {
+          const F2 h0 = f2(v[0][j], v[0][j + 1]), gj = f2(g[j], g[j + 1]);
+          F2 a, d[2];
+          if constexpr (SWIGLU) swiglu_grad(h0, f2(v[H - 1][j], v[H - 1][j + 1]), a, d[0], d[1]);
+          else gelu_sig_grad(h0, a, d[0]);
+          dot2 = fma2(gj, a, dot2);
+          const F2 wg = w * gj;
+          un2(w * a, o[j], o[j + 1]);
 #pragma unroll
-        for (int m = 0; m < H; ++m) un2(d[m] * wg, x[m][0], x[m][1]);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int c = c0 + 32 * (j + t);
-          if (c < I) {
-#pragma unroll
-            for (int m = 0; m < H; ++m) dh[(r * H + m) * I + c] = from_f32<TD>(x[m][t]);
-            if (wa != nullptr) wa[r * I + c] = from_f32<TD>(o[t]);
-          }
+          for (int m = 0; m < H; ++m) un2(d[m] * wg, v[m][j], v[m][j + 1]);
         }
-      }
+#pragma unroll
+        for (int m = 0; m < H; ++m) store_blocks<F>(dh + (r * H + m) * I + c0, left, v[m]);
+        if (wa != nullptr) store_blocks<F>(wa + r * I + c0, left, o);
+      });
     }
     if (dw != nullptr) {
       float dot, dot1;

@@ -327,7 +327,7 @@ def test_gradients_against_differences(moe, dtype):
 
 
 # ------------------------------------------------------------------ 8 bits
-WIDTHS = [1, 7, 8, 31, 32, 33, 40, 64, 199, 256, 1000, 2056]
+WIDTHS = [1, 7, 8, 31, 32, 33, 40, 64, 199, 256, 257, 511, 545, 1000, 2056]
 
 
 def _special(rows, cols, dtype):
