@@ -1450,7 +1450,7 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
   const bool swiglu = d->act == MOE_ACT_SWIGLU;
   const bool biases = !swiglu && d->has_bias;
   const BwdWs L = backward_layout(d);
-  const int T = d->T, D = d->D, M = d->M, k = d->k, Ha = d->I, Is = d->I_sh;
+  const int T = d->T, D = d->D, M = d->M, k = d->k, Ha = d->I;
   const int n1 = swiglu ? 2 * d->I : d->I;
   const long long pairs = static_cast<long long>(T) * k;
   const long long P = L.rows_pad;
