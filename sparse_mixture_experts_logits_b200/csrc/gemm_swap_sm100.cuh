@@ -91,7 +91,15 @@ constexpr int kSwMaxTile = 256;               // tokens per tile
 // store's rows are 512 bytes long: the copy engine works row by row, and loads
 // and stores of 128-byte rows (a buffer per warp) kept it busy most of a tile.
 constexpr int kSwRgStages = 5;
-constexpr int kSwPrefetchKb = 6;
+// What a tile is added onto comes into L2 before the reducing stores ask for
+// it: tiles of up to kSwPrefetchKb k-blocks at their start, by the epilogue
+// warps, longer ones a tile ahead and spread over time, by the MMA warp of the
+// pair's second CTA, which has nothing else to do (a burst of prefetches
+// delays the operand loads behind it).  48 experts x 2048 x 5120, whose bytes
+// alone take 0.62 ms: 256 rows each 0.82 -> 0.66 ms (spread: 0.79); 512 rows
+// 0.86 -> 0.81 (at the start: 0.92); 768 rows 1.00 -> 0.93.
+constexpr int kSwPrefetchKb = 5;
+constexpr int kSwPrefetchGapNs = 60;
 constexpr int kSwRgBufs = 3;  // see the barrier count in the epilogue before changing
 constexpr int kSwRgBufRows = 16;
 constexpr int kSwRgBufBytes = kSwRgBufRows * 128 * 4;
@@ -418,6 +426,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
   __shared__ int s_abort;
   __shared__ int s_total;
   __shared__ int s_dyn;
+  __shared__ int s_round;  // kSwWgradRagged: the epilogue's round; negative: done
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -468,6 +477,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       s_tstart[G] = carry;
       s_total = carry;
       s_abort = 0;
+      s_round = 0;
       // Claim tiles dynamically when at least a quarter of the groups with
       // rows are narrow: their tiles stream a whole weight tile for a few
       // rows, at a cost that depends on what runs beside them, which fixed
@@ -645,6 +655,31 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       }
     }
   } else if (warp == 1) {
+    if (LAYOUT == kSwWgradRagged && !leader && args.accumulate) {
+      // ------------------------------------------ prefetch of long tiles' sums
+      // Ends with the epilogue, whose every wait is bounded.
+      for (int rd = 0;;) {
+        const int cur = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_round), 0);
+        const int tile = swap_tile_at(rd, unit, units);
+        if (cur < 0 || tile >= total) break;
+        if (rd > cur + 1) {
+          __nanosleep(200);
+          continue;
+        }
+        const SwapTile t = swap_decode<LAYOUT>(tile, G, s_tstart, s_cnt, args, num_kb);
+        if (t.nkb > kSwPrefetchKb) {
+          const int col0 = t.wt * args.cols_per_tile;
+          const float* rows = static_cast<const float*>(args.out) + static_cast<size_t>(t.g) * args.out_gstride;
+          for (int l = lane; l < kSwMaxTile * 8; l += 32) {  // eight 128-byte lines of each of the tile's rows
+            const int row = l >> 3, c = col0 + (l & 7) * 32;
+            if (row < t.nrows && c < args.out_cols)
+              prefetch_l2(rows + static_cast<size_t>(t.tok0 + row) * args.ldo + c);
+            __nanosleep(kSwPrefetchGapNs);
+          }
+        }
+        ++rd;
+      }
+    }
     if (leader) {
       // -------------------------------------------------------- MMA issuer
       uint32_t it = 0, s = 0, ph = 0;
@@ -780,12 +815,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         // to four pieces of 32 rows (weight gradients: 32 B columns).
         constexpr int kPieces = kSwMaxTile / (32 * kParts);
         if constexpr (kWgrad) {
-          // What a tile of few rows is added onto comes into L2 during its
-          // MMAs, instead of when the reducing stores ask for it at the end
-          // (48 experts x 2048 x 5120, 256 rows each: 0.82 -> 0.66 ms; the
-          // bytes alone are 0.62).  With more rows to a tile the operand
-          // loads behind the prefetches cost more than they gain (512 rows:
-          // 0.86 -> 0.92 ms).
+          if (warp == 2 && lane == 0) *reinterpret_cast<volatile int*>(&s_round) = rd;
           if (args.accumulate && t.nkb <= kSwPrefetchKb && col - lane < args.out_cols) {
             const float* line = static_cast<const float*>(args.out) + gofs + row0 * args.ldo + (col - lane);
 #pragma unroll 1
@@ -1127,6 +1157,9 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       if (!ok) break;
       tc_fence_before();
       mbar_arrive_remote(buf ? tempty1 : tempty0);
+    }
+    if constexpr (LAYOUT == kSwWgradRagged) {
+      if (warp == 2 && lane == 0) *reinterpret_cast<volatile int*>(&s_round) = -1;
     }
     if constexpr (kWgrad) {
       // the staged chunks are read and written before shared memory is released

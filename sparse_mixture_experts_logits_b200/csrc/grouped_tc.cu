@@ -8,7 +8,7 @@
 // (930 TF/s; a cuBLAS batched product of the same size 0.62), the same with
 // uneven segments 0.66, 8 x 2048 rows 0.45 ms (1210 TF/s; 0.42).  Weight
 // gradients write N x K fp32 per expert: 32 x 512 rows x 2048 x 5120 in 0.42
-// ms, 0.57 when added onto.  Few rows: 256 over 160 experts x 5120 x 1536 in
+// ms, 0.53 when added onto.  Few rows: 256 over 160 experts x 5120 x 1536 in
 // 0.34 ms, 5.9 TB/s of weights.
 #include <algorithm>
 
