@@ -39,6 +39,22 @@ bool tmap_bf16(CUtensorMap* map, const void* base, long long rows, int cols, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 [groups, rows, cols], boxes of 64 rows x 64 columns of one group,
+// 128-byte swizzle; what lies behind a group's last row reads as zero, not as
+// the next group's rows.
+bool tmap_bf16_groups(CUtensorMap* map, const void* base, int groups, int rows, int cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(groups)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * 2 * rows};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(kBK), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // fp32 [groups][rows][cols] with row pitch `ld` and group pitch `gstride`
 // elements, boxes of box_cols columns x box_rows rows, no swizzle: the weight-gradient output.
 bool tmap_f32_out(CUtensorMap* map, void* base, int cols, long long rows, int groups, long long ld,
@@ -138,8 +154,12 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   SwapMaps m = {};
   // A: K-major weight rows, or (backward) an MN-major [rows, a_cols] matrix;
   // B: K-major token rows (128-row boxes), or (weight gradients) MN-major.
-  const int a_inner = L.layout == kSwFwd ? L.K : L.a_cols;
-  if (!tmap_bf16(&m.w, L.W, L.w_rows, a_inner, 64)) return cudaErrorInvalidValue;
+  if (L.layout == kSwDgrad) {
+    if (L.w_rows != static_cast<long long>(L.num_groups) * L.K) return cudaErrorInvalidValue;
+    if (!tmap_bf16_groups(&m.w, L.W, L.num_groups, L.K, L.a_cols)) return cudaErrorInvalidValue;
+  } else if (!tmap_bf16(&m.w, L.W, L.w_rows, L.layout == kSwFwd ? L.K : L.a_cols, 64)) {
+    return cudaErrorInvalidValue;
+  }
   if (is_wgrad(L.layout)) {
     if (!tmap_bf16(&m.x[0], L.X, L.x_rows, L.b_cols, 64)) return cudaErrorInvalidValue;
     if (L.layout == kSwWgradRagged) {
@@ -179,7 +199,6 @@ cudaError_t launch_gemm_swap(const SwapLaunch& L, cudaStream_t s) {
   a.bias = static_cast<const __nv_bfloat16*>(L.bias);
   a.addend = static_cast<const __nv_bfloat16*>(L.addend);
   a.status = L.status;
-  a.k_rows_per_group = L.k_rows_per_group;
   a.b_tiles = L.b_tiles;
   a.b_cols = L.b_cols;
   a.out_gstride = L.out_gstride;

@@ -38,10 +38,11 @@
 // index):
 //   kSwFwd    A = weight rows, K-major ([rows, K], the forward GEMMs);
 //             B = token rows, K-major; groups split the token rows.
-//   kSwDgrad  A = a weight stack read MN-major: group g's K rows are
-//             g * k_rows_per_group + k of a [G * K, A_cols] matrix (W2 or
-//             W1 of the nn.Linear layout contracted over its out index, the
-//             input gradients of the backward); B and groups as kSwFwd.
+//   kSwDgrad  A = a weight stack read MN-major: group g's K rows of a
+//             [G, K, A_cols] tensor, of which a k-block behind the K-th reads
+//             zeros (0 times a NaN in the next group's weights would be one)
+//             (W2 or W1 of the nn.Linear layout contracted over its out index,
+//             the input gradients of the backward); B and groups as kSwFwd.
 //   kSwWgrad  A and B both MN-major activations [rows, cols] and the groups
 //             split the contraction (the rows): group g (segment offsets[g]
 //             .. offsets[g+1], a multiple of 64 rows whose padding rows are
@@ -165,9 +166,8 @@ struct SwapArgs {
   const __nv_bfloat16* bias;   // EPI_GELU_BIAS / EPI_SCALE_BIAS / EPI_BIAS_ADD: [G, out_cols] or nullptr
   const __nv_bfloat16* addend; // EPI_BIAS_ADD: [rows, ldo] or nullptr
   int* status;
-  // kSwDgrad: K rows of A per group.  kSwWgrad: B tiles per group, valid B
-  // columns (output rows) and output elements per group.
-  int k_rows_per_group;
+  // kSwWgrad: B tiles per group, valid B columns (output rows) and output
+  // elements per group.
   int b_tiles;
   int b_cols;
   long long out_gstride;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       // A: kSwFwd weight rows; otherwise the first of this CTA's 128 A columns
       const int w_base = (LAYOUT == kSwFwd ? t.g * args.w_rows_per_group : 0) + t.wt * args.w_tile_step +
                          static_cast<int>(rank) * args.w_cta_step;
-      const int k_row0 = LAYOUT == kSwDgrad ? t.g * args.k_rows_per_group : s_off[t.g];
+      const int k_row0 = s_off[t.g];  // weight gradients: the segment's first row
       int box = 0;
       if constexpr (!kBMn) {
         while (box + 1 < kSwBoxes && swap_box_rows(box + 1) * 2 >= t.n) ++box;
@@ -637,8 +637,11 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
             if constexpr (!kAMn) {
               tma_load_2d_pair(ai, &maps.w, full_leader, kc, w_base);
               tma_load_2d_pair(ai + 64 * kBK * 2, &maps.w, full_leader, kc, w_base + args.w_hi_offset);
-            } else {
+            } else if constexpr (LAYOUT == kSwDgrad) {
               // two boxes of 64 A columns x 64 K rows (8 KB each, 8 KB apart)
+              tma_load_3d_pair(ai, &maps.w, full_leader, w_base, kc, t.g);
+              tma_load_3d_pair(ai + 64 * kBK * 2, &maps.w, full_leader, w_base + args.w_hi_offset, kc, t.g);
+            } else {
               tma_load_2d_pair(ai, &maps.w, full_leader, w_base, k_row0 + kc);
               tma_load_2d_pair(ai + 64 * kBK * 2, &maps.w, full_leader, w_base + args.w_hi_offset, k_row0 + kc);
             }

@@ -134,7 +134,6 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;
     S.X = L.dy; S.x_rows = L.rows;
     S.K = L.N;
-    S.k_rows_per_group = L.N;
     S.a_cols = L.K;
     S.out_cols = L.K; S.ldo = L.K;
   } else {

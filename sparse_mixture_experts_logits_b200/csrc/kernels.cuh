@@ -90,7 +90,6 @@ struct SwapLaunch {
   int* status;
   // backward layouts and epilogues (see SwapArgs)
   int a_cols;                // columns of the MN-major A matrix
-  int k_rows_per_group;      // kSwDgrad
   int b_tiles, b_cols;       // kSwWgrad
   long long out_gstride;     // kSwWgrad
   void* out2; void* out3; int ldo2;

@@ -1217,7 +1217,6 @@ moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* 
     }
     SwapLaunch sb = bwd_swap(kept ? EPI_KEPT_SWIGLU_DACT : EPI_BWD_SWIGLU_DACT, kSwDgrad, w->sh_w2, D, dy, T, D, 1, nullptr, nullptr, T, Is, dhsb,
                              2 * Is, status);
-    sb.k_rows_per_group = D;
     sb.aux = hsb;
     sb.ld_aux = 2 * Is;
     sb.half_cols = Is;
@@ -1228,7 +1227,6 @@ moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* 
     MOE_CUDA(launch_gemm_swap(sb, s));
     SwapLaunch sc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->sh_w1, 2ll * Is, dhsb, T, 2 * Is, 1, nullptr, nullptr, T,
                              D, dxs, D, status);
-    sc.k_rows_per_group = 2 * Is;
     MOE_CUDA(launch_gemm_swap(sc, s));
     SwapLaunch sd = bwd_swap(EPI_STORE_F32, kSwWgrad, asb, T, dy, T, 0, 1, nullptr, nullptr, T, Is, g->dsh_w2, Is,
                              status);
@@ -1392,7 +1390,6 @@ moe_status_t saved_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w
     Range r("moe.experts_backward");
     SwapLaunch gb = bwd_swap(swiglu ? EPI_KEPT_SWIGLU_DACT : EPI_KEPT_GELU_DACT, kSwDgrad, w->w2, 1ll * M * D, dyp,
                              pairs, D, M, offsets, nullptr, pairs, Ha, dh, n1, status);
-    gb.k_rows_per_group = D;
     gb.keep_q = at<int8_t*>(ckpt, C.q);
     gb.keep_e = at<uint8_t*>(ckpt, C.e);
     gb.half_cols = Ha;
@@ -1404,7 +1401,6 @@ moe_status_t saved_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w
     MOE_CUDA(launch_gemm_swap(gb, s));
     SwapLaunch gc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->w1, 1ll * M * n1, dh, pairs, n1, M, offsets, nullptr, pairs, D,
                              dxp, D, status);
-    gc.k_rows_per_group = n1;
     MOE_CUDA(launch_gemm_swap(gc, s));
     GroupedLaunch gd{};
     gd.dir = kGroupedWgrad;
@@ -1527,7 +1523,6 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
     // G = dy W2 (W2 read MN-major); dh = w G act'(h); per-32-column <G, a>
     SwapLaunch gb = bwd_swap(swiglu ? EPI_BWD_SWIGLU_DACT : EPI_BWD_GELU_DACT, kSwDgrad, w->w2, 1ll * M * D, dypp,
                              P, D, M, offp, counts, P, Ha, dhb, n1, status);
-    gb.k_rows_per_group = D;
     gb.aux = hpb;
     gb.ld_aux = n1;
     gb.half_cols = Ha;
@@ -1538,7 +1533,6 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
     // dx rows = dh W1 (W1 read MN-major), fp32
     SwapLaunch gc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->w1, 1ll * M * n1, dhb, P, n1, M, offp, counts, P, D, dxpp,
                              D, status);
-    gc.k_rows_per_group = n1;
     MOE_CUDA(launch_gemm_swap(gc, s));
     // weight gradients over each expert's padded segment
     SwapLaunch gd = bwd_swap(EPI_STORE_F32, kSwWgrad, awb, P, dypp, P, 0, M, offp, nullptr, P, Ha, g->dw2, Ha,

@@ -104,6 +104,31 @@ def check(B, cfg):
     return inp, dy, layer, ck, y, g
 
 
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("name", ["glam_small_bf16", "glm_small_bf16"])
+def test_bad_weights_stay_alone(B, name, saved):
+    """NaN in one expert's weights leaves the other experts' weight gradients
+    as they were, at widths that end inside a block of 64."""
+    cfg = dict(ms.get_config(name), D=272, I=144)
+    inp = gpu_inputs(cfg)
+    dy = ms.upstream_grad(cfg, "cuda")
+
+    def grads(inp):
+        layer = B.MoELayer(cfg, inp)
+        ck = B.LayerCheckpoint(layer) if saved else None
+        layer.forward(inp["x"], checkpoint=ck)
+        return layer.backward(inp["x"], dy, checkpoint=ck)
+
+    clean, bad = grads(inp), cfg["M"] // 2
+    inp2 = dict(inp, w1=inp["w1"].clone(), w2=inp["w2"].clone())
+    inp2["w1"][bad] = float("nan")
+    inp2["w2"][bad] = float("nan")
+    got = grads(inp2)
+    rest = [g for g in range(cfg["M"]) if g != bad]
+    for key in ("dw1", "dw2"):
+        assert torch.equal(got[key][rest], clean[key][rest]), key
+
+
 @pytest.mark.parametrize("name", ["glam_tiny_f32", "glam_small_bf16", "glm_small_bf16", "glm_small_f32",
                                   "glm_grouped_bf16", "glm_grouped_f32", "glam_nonorm_f32", "glm_medium_bf16"])
 def test_layer_from_its_checkpoint(B, name):

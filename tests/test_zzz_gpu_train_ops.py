@@ -125,6 +125,30 @@ def test_a_bad_expert_stays_alone(moe, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(72, 80), (8, 136), (200, 264)])
+def test_bad_weights_stay_alone(moe, N, K, dtype):
+    """NaN and infinity in one expert's weights and bias reach no other expert's
+    rows, although the contraction over N ends inside a block of 64."""
+    counts = [5, 30, 70, 1, 64, 9]
+    offsets = _offsets(counts)
+    rows = int(offsets[-1])
+    x, dy = _randn(1, (rows, K), DT[dtype]), _randn(2, (rows, N), DT[dtype])
+    w, bias = _randn(3, (6, N, K), DT[dtype]), _randn(4, (6, N), DT[dtype])
+    off = _dev(offsets)
+    op = moe.GroupedLinear(w, rows, bias=bias)
+    clean = op.forward(x, off), op.input_grad(dy, off)
+    for bad, value in ((1, float("nan")), (3, float("inf")), (5, -float("inf"))):
+        w2, bias2 = w.clone(), bias.clone()
+        w2[bad], bias2[bad] = value, value
+        op2 = moe.GroupedLinear(w2, rows, bias=bias2)
+        y, dx = op2.forward(x, off), op2.input_grad(dy, off)
+        b, e = offsets[bad], offsets[bad + 1]
+        rest = torch.cat([torch.arange(0, b), torch.arange(e, rows)])
+        assert torch.equal(y[rest], clean[0][rest]) and torch.equal(dx[rest], clean[1][rest])
+        assert not y[b:e].isfinite().any() and not dx[b:e].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_offsets_that_are_no_dispatch_stay_inside(moe, dtype):
     """Bounds outside [0, rows] are clamped, a segment that ends before it starts is empty."""
     rows, N, K = 100, 40, 48
