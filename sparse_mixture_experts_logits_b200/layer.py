@@ -107,6 +107,8 @@ class MoELayer:
         base = self.ws.data_ptr()
         self._ws_off = (-base) % 256
         self.layout = abi.moe_workspace_layout(self.desc)
+        self._fwd = (self.ws, self._ws_off)  # the last forward's workspace
+        self._fwd_kept = False
         self._bws = None
         self._save = None
         self._cws = None
@@ -127,10 +129,14 @@ class MoELayer:
             if self._save is None:
                 nbytes = abi.moe_forward_save_workspace_size(self.desc)
                 # a bf16 layer keeps them from its own workspace
-                self._save = (self.ws_ptr, self.ws_bytes, None) if nbytes <= self.ws_bytes else self._scratch(nbytes, stream)
+                self._save = ((self.ws, self._ws_off, self.ws_bytes) if nbytes <= self.ws_bytes
+                              else self._scratch(nbytes, stream))
+            buf, off, nbytes = self._save
             abi.moe_forward_save(self.desc, self.weights, x.data_ptr(), _ptr(addend), y.data_ptr(), checkpoint.ptr,
-                                 checkpoint.nbytes, self._save[0], self._save[1], _stream_handle(stream))
+                                 checkpoint.nbytes, buf.data_ptr() + off, nbytes, _stream_handle(stream))
+            self._fwd, self._fwd_kept = (buf, off), True
             return y
+        self._fwd, self._fwd_kept = (self.ws, self._ws_off), False
         if addend is None:
             abi.moe_forward(self.desc, self.weights, x.data_ptr(), y.data_ptr(), self.ws_ptr, self.ws_bytes,
                             _stream_handle(stream))
@@ -140,13 +146,14 @@ class MoELayer:
         return y
 
     def _scratch(self, nbytes: int, stream):
-        """(256-byte aligned address, bytes, buffer), allocated on the stream that will use it"""
+        """(buffer, offset of its first 256-byte boundary, bytes), allocated on the stream that will use it"""
         with torch.cuda.stream(stream):
             buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
-        return buf.data_ptr() + (-buf.data_ptr()) % 256, nbytes, buf
+        return buf, (-buf.data_ptr()) % 256, nbytes
 
     def device_status(self, stream=None) -> int:
-        return abi.moe_device_status(self.ws_ptr, _stream_handle(stream))
+        """The status of the last forward."""
+        return abi.moe_device_status(self._fwd[0].data_ptr() + self._fwd[1], _stream_handle(stream))
 
     def grad_shapes(self) -> dict:
         """Shapes of the gradients moe_backward writes (None: not written)."""
@@ -185,9 +192,10 @@ class MoELayer:
         for name in abi.Grads._fields_:
             setattr(g, name[0], _ptr(grads.get(name[0])))
         if checkpoint is not None:
-            self._last_bws = self._cws[0]
+            buf, off, nbytes = self._cws
+            self._last_bws = buf.data_ptr() + off
             abi.moe_backward_saved(self.desc, self.weights, x.data_ptr(), dy.data_ptr(), checkpoint.ptr,
-                                   checkpoint.nbytes, g, self._cws[0], self._cws[1], _stream_handle(stream))
+                                   checkpoint.nbytes, g, self._last_bws, nbytes, _stream_handle(stream))
             return grads
         self._last_bws = self._bws.data_ptr() + self._bws_off
         abi.moe_backward(self.desc, self.weights, x.data_ptr(), dy.data_ptr(), g, self._last_bws, self.bws_bytes,
@@ -199,7 +207,9 @@ class MoELayer:
         return abi.moe_device_status(self._last_bws, _stream_handle(stream))
 
     def backward_view(self, name: str) -> torch.Tensor:
-        """The routing intermediate ``name`` of the last backward."""
+        """The routing intermediate ``name`` that the last backward recomputed."""
+        if self._bws is None or self._last_bws != self._bws.data_ptr() + self._bws_off:
+            raise RuntimeError("the last backward recomputed no routing: from a checkpoint it is the checkpoint's")
         return self.view(name, ws=(self._bws, self._bws_off))
 
     def view(self, name: str, dtype=None, ws=None) -> torch.Tensor:
@@ -214,7 +224,9 @@ class MoELayer:
             "out_perm": ((pairs, d.D), torch.float32),
         }
         shape, dt = shapes[name]
-        buf, base = (self.ws, self._ws_off) if ws is None else ws
+        if ws is None and self._fwd_kept and name in ("topk_idx", "topk_w"):
+            raise RuntimeError(f"the last forward kept {name} in its checkpoint")
+        buf, base = self._fwd if ws is None else ws
         off = base + getattr(self.layout, name)
         n = 1
         for s in shape:

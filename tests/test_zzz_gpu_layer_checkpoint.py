@@ -180,6 +180,30 @@ def test_two_checkpoints_of_one_layer(B):
     assert not torch.equal(g1["dx"], g2["dx"])
 
 
+@pytest.mark.parametrize("name", ["glm_small_bf16", "glm_small_f32"])
+def test_views_and_status_follow_the_last_call(B, name):
+    """The views and the status are those of the workspace that the last forward or backward used; what a
+    checkpoint holds in their place is not read from an older pass."""
+    cfg = ms.get_config(name)
+    inp = gpu_inputs(cfg)
+    layer = B.MoELayer(cfg, inp)
+    with pytest.raises(RuntimeError, match="checkpoint"):
+        layer.backward_view("topk_idx")
+    _, dy, _, ck, _, _ = run(B, cfg, layer=layer, inp=inp)
+    for view in (layer.view, layer.backward_view):
+        with pytest.raises(RuntimeError, match="checkpoint"):
+            view("topk_idx")
+    kept = {n: layer.view(n).clone() for n in ("counts", "offsets", "slot_of", "row_token")}
+    assert kept["counts"].sum() == cfg["T"] * cfg["k"]
+    layer.view("status").fill_(3)
+    assert layer.device_status() == 3 and layer.device_status() == 0
+    layer.forward(inp["x"])
+    assert torch.equal(layer.view("topk_idx"), ck.view("topk_idx"))
+    assert all(torch.equal(layer.view(n), v) for n, v in kept.items())
+    layer.backward(inp["x"], dy)
+    assert torch.equal(layer.backward_view("topk_idx"), ck.view("topk_idx"))
+
+
 def test_captured_and_replayed(B):
     """Forward and backward in one graph, replayed on another input: bit for bit the eager step."""
     cfg = ms.get_config("glm_small_bf16")
