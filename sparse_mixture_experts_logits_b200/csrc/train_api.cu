@@ -150,7 +150,7 @@ moe_status_t moe_ckpt_dequantize(const int8_t* q, const uint8_t* e, const int32_
   MOE_TRY(check_act(rows, cols, MOE_ACT_GELU_TANH, dtype, dtype));
   if (src_rows < 0) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!q || !e || !dst) return MOE_ERR_INVALID_ARG;
+  if ((src_rows > 0 && (!q || !e)) || !dst) return MOE_ERR_INVALID_ARG;
   if (row_index == nullptr && rows > src_rows) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_device());
   return cuda_status(launch_ckpt_dequantize(dtype, q, e, row_index, n_rows, rows, src_rows, cols, dst, device_status,

@@ -259,6 +259,17 @@ def test_what_the_handles_refuse(moe):
         c.load(torch.zeros(2, 2, dtype=torch.int32, device="cuda"))
 
 
+@pytest.mark.parametrize("cols", [40, 33])
+def test_a_checkpoint_without_rows(moe, cols):
+    """Every index lies outside it: zero rows and the status."""
+    c = moe.RowCheckpoint(0, cols, torch.bfloat16)
+    c.save(torch.empty(0, cols, dtype=torch.bfloat16, device="cuda"))
+    assert c.load().shape == (0, cols)
+    out = torch.full((3, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.load(_dev([0, -1, 5]), out=out)
+    assert not out.any() and c.status.item() != 0
+
+
 @pytest.mark.parametrize("act", ["swiglu", "gelu_tanh"])
 def test_checkpoints_off_their_boundaries(moe, act):
     """Contiguous tensors that start anywhere: the same bits as on whole boundaries."""
