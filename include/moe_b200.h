@@ -487,7 +487,7 @@ int moe_backward_launch_count(const moe_layer_desc_t* d);
  * magnitude in h's block of 32. */
 
 /* Bytes of a checkpoint (256-byte aligned, caller-owned); 0 if the descriptor
- * is invalid. */
+ * is invalid.  Limit of every function here: T k < 2^30 (MOE_ERR_UNSUPPORTED). */
 size_t moe_checkpoint_size(const moe_layer_desc_t* d);
 
 /* Byte offsets of a checkpoint's parts, into out[MOE_CHECKPOINT_PARTS]:

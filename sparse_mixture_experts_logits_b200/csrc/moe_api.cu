@@ -1790,10 +1790,18 @@ int moe_backward_launch_count(const moe_layer_desc_t* d) {
 
 // ------------------------------------------------- training with a checkpoint
 
-size_t moe_checkpoint_size(const moe_layer_desc_t* d) { return check_desc(d) == MOE_OK ? ckpt_layout(d).total : 0; }
+// A SwiGLU row is kept as two rows, which are counted in 31 bits.
+static moe_status_t check_ckpt_desc(const moe_layer_desc_t* d) {
+  MOE_TRY(check_desc(d));
+  return static_cast<long long>(d->T) * d->k >= (1 << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+size_t moe_checkpoint_size(const moe_layer_desc_t* d) {
+  return check_ckpt_desc(d) == MOE_OK ? ckpt_layout(d).total : 0;
+}
 
 moe_status_t moe_checkpoint_offsets(const moe_layer_desc_t* d, size_t* out) {
-  MOE_TRY(check_desc(d));
+  MOE_TRY(check_ckpt_desc(d));
   if (out == nullptr) return MOE_ERR_INVALID_ARG;
   const CkptLayout C = ckpt_layout(d);
   const size_t parts[MOE_CHECKPOINT_PARTS] = {C.idx, C.tw, C.logits, C.q, C.e, C.sq, C.se};
@@ -1811,12 +1819,12 @@ static size_t forward_save_ws(const moe_layer_desc_t* d, size_t* h_at) {
 
 size_t moe_forward_save_workspace_size(const moe_layer_desc_t* d) {
   size_t at_h;
-  return check_desc(d) == MOE_OK ? forward_save_ws(d, &at_h) : 0;
+  return check_ckpt_desc(d) == MOE_OK ? forward_save_ws(d, &at_h) : 0;
 }
 
 moe_status_t moe_forward_save(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* addend,
                               void* y, void* ckpt, size_t ckpt_bytes, void* ws, size_t ws_bytes, void* stream) {
-  MOE_TRY(check_desc(d));
+  MOE_TRY(check_ckpt_desc(d));
   if (d->T > 0) {
     size_t at_h;
     if (!ckpt || !aligned_ws(ckpt) || !ws || !aligned_ws(ws)) return MOE_ERR_INVALID_ARG;
@@ -1830,13 +1838,13 @@ moe_status_t moe_forward_save(const moe_layer_desc_t* d, const moe_weights_t* w,
 }
 
 size_t moe_backward_saved_workspace_size(const moe_layer_desc_t* d) {
-  return check_desc(d) == MOE_OK ? saved_layout(d).total : 0;
+  return check_ckpt_desc(d) == MOE_OK ? saved_layout(d).total : 0;
 }
 
 moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
                                 const void* ckpt, size_t ckpt_bytes, const moe_grads_t* grads, void* ws,
                                 size_t ws_bytes, void* stream) {
-  MOE_TRY(check_desc(d));
+  MOE_TRY(check_ckpt_desc(d));
   if (d->T > 0 && (!ckpt || !aligned_ws(ckpt) || ckpt_bytes < ckpt_layout(d).total)) return MOE_ERR_INVALID_ARG;
   return backward_impl(d, w, x, dy, grads, ws, ws_bytes, static_cast<cudaStream_t>(stream),
                        const_cast<void*>(ckpt));

@@ -139,5 +139,14 @@ def test_layer_checkpoint_refuses(moe):
     for fn in (moe.moe_checkpoint_size, moe.moe_forward_save_workspace_size, moe.moe_backward_saved_workspace_size):
         assert fn(bad) == 0
     assert _status(moe, moe.moe_checkpoint_offsets, bad) == 1
+    many, w, g = _layer(moe)   # 2^30 (token, expert) pairs: a SwiGLU row is kept as two, counted in 31 bits
+    many.M, many.k, many.D, many.I, many.I_sh, many.n_group, many.T = 63, 32, 16, 16, 0, 0, (1 << 25) - 1
+    assert moe.moe_checkpoint_size(many) > 0
+    many.T += 1
+    assert moe.moe_workspace_size(many) > 0
+    for fn in (moe.moe_checkpoint_size, moe.moe_forward_save_workspace_size, moe.moe_backward_saved_workspace_size):
+        assert fn(many) == 0
+    assert _status(moe, moe.moe_forward_save, many, w, P, None, P, P, 1 << 60, P, 1 << 60) == 2
+    assert _status(moe, moe.moe_backward_saved, many, w, P, P, P, 1 << 60, g, P, 1 << 60) == 2
     zero, w, _ = _layer(moe, T=0)
     moe.moe_forward_save(zero, w, None, None, None, None, 0, None, 0)
