@@ -660,15 +660,18 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
   } else if (warp == 1) {
     if (LAYOUT == kSwWgradRagged && !leader && args.accumulate) {
       // ------------------------------------------ prefetch of long tiles' sums
-      // Ends with the epilogue, whose every wait is bounded.
-      for (int rd = 0;;) {
+      // Ends with the epilogue, whose every wait is bounded, or without a
+      // result after some seconds of one tile: a hint that nothing waits for.
+      for (int rd = 0, waits = 0;;) {
         const int cur = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_round), 0);
         const int tile = swap_tile_at(rd, unit, units);
         if (cur < 0 || tile >= total) break;
         if (rd > cur + 1) {
+          if (++waits > (1 << 24)) break;
           __nanosleep(200);
           continue;
         }
+        waits = 0;
         const SwapTile t = swap_decode<LAYOUT>(tile, G, s_tstart, s_cnt, args, num_kb);
         if (t.nkb > kSwPrefetchKb) {
           const int col0 = t.wt * args.cols_per_tile;
