@@ -4,7 +4,10 @@
 // the three products of a linear layer over ragged row segments:
 //   forward   y[r, n]   = sum_k x[r, k]  W_g[n, k] (+ b_g[n])
 //   dgrad     dx[r, k]  = sum_n dy[r, n] W_g[n, k]
-//   wgrad     dW_g[n,k] = sum_r dy[r, n] x[r, k]     over g's rows
+//   wgrad     dW_g[n,k] = sum_r dy[r, n] x[r, k]     over g's rows, and with
+//             it db_g[n] = sum_r dy[r, n]: the tiles of the first columns have
+//             dy's slices in shared memory, and each of their 16 threads of a
+//             row block adds up one of a slice's 16 steps
 // 64 x 64 output tiles, 16-deep slices through shared memory (fp32: four
 // stages of 4-byte asynchronous copies, which suit any width and alignment;
 // bf16: the next slice through registers), a 4 x 4 block of neighbouring sums per
@@ -14,7 +17,6 @@
 // the tensor cores: 30 experts x 50 rows x 390 x 380 in 33 us (14 TF/s).
 #include <algorithm>
 
-#include "grouped_colsum.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -45,6 +47,7 @@ struct Args {
   int Kc;       // contraction length (forward, dgrad)
   int col_tiles;
   int accumulate;
+  float* db;    // wgrad: [G, M] column sums of A, or null
   int* status;  // cleared by the first block (nothing here sets it)
 };
 
@@ -98,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_simt_kernel(const Args p)
     const long long c0 = WGRAD ? seg0 : 0, c1 = WGRAD ? seg1 : p.Kc;
     const long long bg = static_cast<long long>(g) * p.b_gstride;
     float acc[4][4] = {}, tot[4][4] = {};
+    const bool sums = WGRAD && p.db != nullptr && n0 == 0;
+    float4 colsum = make_float4(0.f, 0.f, 0.f, 0.f);  // of the steps that are tx modulo 16
     int slices = 0;
     // This thread's elements of a slice, along each operand's contiguous
     // index: four of A and four of B.  Their addresses in the first slice, and for each how many
@@ -180,6 +185,10 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_simt_kernel(const Args p)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
       }
+      if (WGRAD && sums) {
+        const float4 v = *reinterpret_cast<const float4*>(&As[st][tx][4 * ty]);
+        colsum.x += v.x; colsum.y += v.y; colsum.z += v.z; colsum.w += v.w;
+      }
       if (++slices == kChunkSlices) {
         slices = 0;
 #pragma unroll
@@ -190,6 +199,17 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_simt_kernel(const Args p)
     }
     if constexpr (kAsync) copies_wait<0>();
     __syncthreads();  // the tile's stages are read before the next tile fills them
+    if (WGRAD && sums) {
+      float v[4] = {colsum.x, colsum.y, colsum.z, colsum.w};
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      float* out = p.db + static_cast<long long>(g) * p.M + m0 + 4 * ty;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (tx == 0 && 4 * ty + i < nm) out[i] = p.accumulate ? out[i] + v[i] : v[i];
+    }
     const long long cg = WGRAD ? static_cast<long long>(g) * p.c_gstride : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -206,26 +226,6 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_simt_kernel(const Args p)
         *dst = from_f32<TO>(v);
       }
     }
-  }
-}
-
-template <typename T, bool PAIRED>
-__global__ void __launch_bounds__(256) grouped_colsum_kernel(const T* __restrict__ dy,
-                                                             const int32_t* __restrict__ offsets, int rows, int N,
-                                                             int accumulate, float* __restrict__ out) {
-  __shared__ float2 s[8][32];
-  grouped_colsum_block<T, PAIRED>(dy, offsets, rows, N, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, accumulate,
-                                  out + (static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y) * N, s);
-}
-
-__global__ void __launch_bounds__(256) grouped_colsum_join_kernel(const float* __restrict__ part, int shares,
-                                                                  long long n, int accumulate,
-                                                                  float* __restrict__ db) {
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    float v = accumulate ? db[i] : 0.f;
-    for (int z = 0; z < shares; ++z) v += part[z * n + i];
-    db[i] = v;
   }
 }
 
@@ -251,6 +251,7 @@ cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_
     a.C = L.out; a.ldc = L.K; a.c_gstride = NK;
     a.M = L.N; a.N = L.K;
     a.accumulate = L.accumulate;
+    a.db = L.db;
   } else if (L.dir == kGroupedDgrad) {
     a.A = L.dy; a.a_sm = L.N; a.a_sc = 1;
     a.B = L.w; a.b_sn = 1; a.b_sc = L.K; a.b_gstride = NK;
@@ -272,36 +273,6 @@ cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_
   const long long tiles = (L.rows / kTM + std::min<long long>(L.G, L.rows)) * a.col_tiles;
   if (bf) return obf ? run<__nv_bfloat16, __nv_bfloat16, false>(a, tiles, s) : run<__nv_bfloat16, float, false>(a, tiles, s);
   return run<float, float, false>(a, tiles, s);
-}
-
-int grouped_colsum_shares(int G, int rows, int N) {
-  const long long blocks = static_cast<long long>((N + 63) / 64) * G;
-  // eight blocks an SM, of 128 rows of an even segment at least
-  const long long want = (8ll * 148 + blocks - 1) / blocks, most = (static_cast<long long>(rows) / G + 127) / 128;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>({want, most, 64})));
-}
-
-cudaError_t launch_grouped_colsum(const GroupedLaunch& L, cudaStream_t s) {
-  const int shares = grouped_colsum_shares(L.G, L.rows, L.N);
-  const dim3 grid((L.N + 63) / 64, L.G, shares);
-  float* out = shares > 1 ? L.part : L.db;
-  const int acc = shares > 1 ? 0 : L.accumulate;
-  const bool pair = L.N % 2 == 0 && reinterpret_cast<uintptr_t>(L.dy) % 8 == 0;
-  if (L.dtype == MOE_DTYPE_BF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(L.dy);
-    if (pair) grouped_colsum_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
-    else grouped_colsum_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
-  } else {
-    const float* p = static_cast<const float*>(L.dy);
-    if (pair) grouped_colsum_kernel<float, true><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
-    else grouped_colsum_kernel<float, false><<<grid, 256, 0, s>>>(p, L.offsets, L.rows, L.N, acc, out);
-  }
-  if (shares > 1) {
-    const long long n = static_cast<long long>(L.G) * L.N;
-    const int blocks = static_cast<int>(std::min<long long>((n + 255) / 256, 4ll * num_sms()));
-    grouped_colsum_join_kernel<<<blocks, 256, 0, s>>>(L.part, shares, n, L.accumulate, L.db);
-  }
-  return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -13,7 +13,6 @@
 #include <algorithm>
 
 #include "gemm_sm100.cuh"
-#include "grouped_colsum.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -23,6 +22,83 @@ constexpr size_t kHead = 256;  // status word and tile counters
 constexpr int kTail = kBK;     // rows of a group's tail buffer: one k-block
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// db[g, n] (+)= sum over g's rows of dy[r, n] (N even).  A block of 256
+// threads takes share `z` of `shares` of group g's rows for the 64 columns of
+// column tile `nt`: its eight warps take every eighth row, two columns a
+// thread and eight rows in flight, and their sums are added in warp order.
+// With more than one share the blocks leave partial sums, which a second
+// kernel adds in order.  Bound by reading dy once.  `out`: group g's N sums
+// (or the share's partial ones); `s`: shared memory.
+__device__ __forceinline__ void colsum_block(const __nv_bfloat16* __restrict__ dy, const int32_t* __restrict__ offsets,
+                                             int rows, int N, int nt, int g, int z, int shares, int accumulate,
+                                             float* __restrict__ out, float2 (*s)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = max(0, min(offsets[g], rows)), e = max(b, max(0, min(offsets[g + 1], rows)));
+  const int per = (e - b + shares - 1) / shares;
+  const int r0 = static_cast<int>(min(static_cast<long long>(e), b + static_cast<long long>(z) * per));
+  const int r1 = min(e, r0 + per);
+  const int n = nt * 64 + 2 * lane;
+  float2 a = make_float2(0.f, 0.f);
+  if (n < N) {
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(dy + static_cast<long long>(r0 + warp) * N + n);
+    const long long step = 4ll * N;
+    int r = r0 + warp;
+    for (; r + 56 < r1; r += 64, p += 8 * step) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __bfloat1622float2(p[i * step]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) { a.x += v[i].x; a.y += v[i].y; }
+    }
+    for (; r < r1; r += 8, p += step) {
+      const float2 v = __bfloat1622float2(*p);
+      a.x += v.x;
+      a.y += v.y;
+    }
+  }
+  __syncthreads();  // `s` of an earlier tile is read
+  s[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0 && n < N) {
+    float2 v = s[0][lane];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) { v.x += s[i][lane].x; v.y += s[i][lane].y; }
+    out[n] = accumulate ? out[n] + v.x : v.x;
+    out[n + 1] = accumulate ? out[n + 1] + v.y : v.y;
+  }
+}
+
+__global__ void __launch_bounds__(256) colsum_kernel(const __nv_bfloat16* __restrict__ dy,
+                                                     const int32_t* __restrict__ offsets, int rows, int N,
+                                                     int accumulate, float* __restrict__ out) {
+  __shared__ float2 s[8][32];
+  colsum_block(dy, offsets, rows, N, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, accumulate,
+               out + (static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y) * N, s);
+}
+
+__global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int shares, long long n,
+                                                          int accumulate, float* __restrict__ db) {
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    float v = accumulate ? db[i] : 0.f;
+    for (int z = 0; z < shares; ++z) v += part[z * n + i];
+    db[i] = v;
+  }
+}
+
+cudaError_t launch_colsum(const GroupedLaunch& L, cudaStream_t s) {
+  const int shares = grouped_colsum_shares(L.G, L.rows, L.N);
+  colsum_kernel<<<dim3((L.N + 63) / 64, L.G, shares), 256, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(L.dy), L.offsets, L.rows, L.N, shares > 1 ? 0 : L.accumulate,
+      shares > 1 ? L.part : L.db);
+  if (shares > 1) {
+    const long long n = static_cast<long long>(L.G) * L.N;
+    const int blocks = static_cast<int>(std::min<long long>((n + 255) / 256, 4ll * num_sms()));
+    colsum_join_kernel<<<blocks, 256, 0, s>>>(L.part, shares, n, L.accumulate, L.db);
+  }
+  return cudaGetLastError();
+}
 
 // Before a ragged weight gradient.  For group g = blockIdx.y with rows
 // [b, e): its last (e - b) % 64 rows of src, filled up with zero rows to 64,
@@ -41,8 +117,8 @@ __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restr
   if (blockIdx.z == 2) {
     __shared__ float2 part[8][32];
     for (int nt = blockIdx.x; nt * 64 < 8 * vn; nt += gridDim.x)
-      grouped_colsum_block<__nv_bfloat16, true>(reinterpret_cast<const __nv_bfloat16*>(dy), offsets, rows, 8 * vn, nt,
-                                                g, 0, 1, accumulate, db + static_cast<long long>(g) * 8 * vn, part);
+      colsum_block(reinterpret_cast<const __nv_bfloat16*>(dy), offsets, rows, 8 * vn, nt, g, 0, 1, accumulate,
+                   db + static_cast<long long>(g) * 8 * vn, part);
     return;
   }
   const int b = max(0, min(offsets[g], rows)), e = max(0, min(offsets[g + 1], rows));
@@ -65,6 +141,13 @@ __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restr
 }  // namespace
 
 bool grouped_tc_ok(int dtype, int N, int K) { return dtype == MOE_DTYPE_BF16 && N % 8 == 0 && K % 8 == 0; }
+
+int grouped_colsum_shares(int G, int rows, int N) {
+  const long long blocks = static_cast<long long>((N + 63) / 64) * G;
+  // eight blocks an SM, of 128 rows of an even segment at least
+  const long long want = (8ll * 148 + blocks - 1) / blocks, most = (static_cast<long long>(rows) / G + 127) / 128;
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({want, most, 64})));
+}
 
 size_t grouped_tc_workspace(int dir, int G, int N, int K) {
   if (dir != kGroupedWgrad) return kHead;
@@ -100,7 +183,7 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (L.db != nullptr && !sums) {
-      e = launch_grouped_colsum(L, s);
+      e = launch_colsum(L, s);
       if (e != cudaSuccess) return e;
     }
     // A = x (the output's contiguous index), B = dy: dw[g][n][k]

@@ -125,8 +125,8 @@ struct GroupedLaunch {
   const void* bias;        // [G, N] or null
   int accumulate;          // wgrad: add onto out
   void* out;
-  // wgrad: the bias gradient db [G, N] (fp32, or null) and, when
-  // grouped_colsum_shares(...) > 1, that many [G, N] of partial sums
+  // wgrad: the bias gradient db [G, N] (fp32, or null) and, on the tensor-core
+  // path, grouped_colsum_shares(...) [G, N] of partial sums if that is > 1
   float* db;
   float* part;
   // Tensor-core path: the status word that waits report to (null: the first
@@ -140,9 +140,7 @@ cudaError_t launch_grouped_simt(const GroupedLaunch& L, int* status, cudaStream_
 bool grouped_tc_ok(int dtype, int N, int K);
 size_t grouped_tc_workspace(int dir, int G, int N, int K);
 cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s);
-// L.db (+)= column sums of dy over each segment.
 int grouped_colsum_shares(int G, int rows, int N);
-cudaError_t launch_grouped_colsum(const GroupedLaunch& L, cudaStream_t s);
 
 // ckpt.cu: activation checkpoints in 8 bits (blocks of MOE_CKPT_BLOCK columns).
 cudaError_t launch_ckpt_quantize(int dtype, const void* src, const int32_t* n_rows, int rows, int cols, int8_t* q,

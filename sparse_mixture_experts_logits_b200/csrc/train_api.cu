@@ -25,13 +25,13 @@ size_t grouped_ws(int dir, int G, int N, int K, int dtype) {
   return grouped_tc_ok(dtype, N, K) ? grouped_tc_workspace(dir, G, N, K) : kAlign;
 }
 
-// moe_grouped_wgrad: that, and the bias gradient's partial sums behind it.
+// moe_grouped_wgrad: that, and (tensor cores) the bias gradient's partial sums behind it.
 struct WgradWs { size_t part, total; };
 WgradWs wgrad_layout(int G, int N, int K, int rows, int dtype) {
   Carve c;
   WgradWs L;
   c.take(grouped_ws(kGroupedWgrad, G, N, K, dtype));
-  const int shares = grouped_colsum_shares(G, rows, N);
+  const int shares = grouped_tc_ok(dtype, N, K) ? grouped_colsum_shares(G, rows, N) : 1;
   L.part = c.take(shares > 1 ? static_cast<size_t>(shares) * G * N * 4 : 0);
   L.total = c.off;
   return L;
@@ -40,8 +40,7 @@ WgradWs wgrad_layout(int G, int N, int K, int rows, int dtype) {
 // Clears the status word first (in the launches themselves).
 moe_status_t run_grouped(const GroupedLaunch& L, void* ws, cudaStream_t s) {
   if (grouped_tc_ok(L.dtype, L.N, L.K)) return cuda_status(launch_grouped_tc(L, ws, s));
-  MOE_CUDA(launch_grouped_simt(L, static_cast<int*>(ws), s));
-  return L.db != nullptr ? cuda_status(launch_grouped_colsum(L, s)) : MOE_OK;
+  return cuda_status(launch_grouped_simt(L, static_cast<int*>(ws), s));
 }
 
 // The arguments that the two row products share.
