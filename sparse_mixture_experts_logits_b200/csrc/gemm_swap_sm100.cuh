@@ -437,6 +437,8 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
   const uint32_t smem_base = (smem_addr(dyn_smem) + 1023u) & ~1023u;
   float* xbuf = reinterpret_cast<float*>(dyn_smem + (smem_base - smem_addr(dyn_smem)) + kSwStages * kSwStageBytes);
   const int G = args.num_groups;
+  // launched while its preparation runs (see launch_swap_epi): nothing is read or written before this
+  if constexpr (LAYOUT == kSwWgradRagged) grid_dependency_wait();
 
   // A call of one small launch saves the separate clear.  No error that
   // another CTA reports can be lost to it: a wait gives up after two seconds,

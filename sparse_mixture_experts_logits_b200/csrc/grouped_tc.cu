@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restr
                                                             uint4* __restrict__ x_tail, uint4* __restrict__ dy_tail,
                                                             uint4* __restrict__ out, float* __restrict__ db,
                                                             int* status) {
+  grid_launch_dependents();
   if (status != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0;
   const int g = blockIdx.y;
   if (blockIdx.z == 2) {
