@@ -16,7 +16,7 @@
 // and written once per form (bf16 or fp32 in, 8 bits + 1/32 byte out).
 // Measured on a B200 whose copies reach 6.5 TB/s, bf16: SwiGLU of 32768 x
 // 2048 saved in 91 us (6.0 TB/s), its backward 109 us (6.2); GELU of 16384 x
-// 8192 118 and 162 us (5.8 TB/s); rows of 8192 x 5120 kept in 27 us and read
+// 8192 113 and 160 us (5.9 TB/s); rows of 8192 x 5120 kept in 27 us and read
 // back four times in 69 us (writes; a plain fill of those bytes takes 88).
 // Widths that are no multiple of 8 run at about half these rates.
 #include <algorithm>
@@ -595,16 +595,23 @@ __global__ void __launch_bounds__(256, 4) act_backward_vec_kernel(const int8_t* 
 }
 
 // Threads along a row (as a power of two) and the grid.  As few as one warp a
-// row where that makes 6 blocks an SM (no block-wide reduction for dw, long
-// runs per thread), up to 256 where there are fewer rows (4097 rows of 8192
-// columns: 513 blocks of one-warp rows leave the SMs unevenly filled).  Of
-// those the most that leave at most an eighth of them idle in the row's last
-// step (192 columns: 8 threads three times, not 32 of which 8 idle).
+// row where that makes 3 blocks an SM (long runs per thread, no block-wide
+// reduction for dw), more where there are fewer rows (2000 x 4096 read back:
+// 64 threads 10.3 us, 32 13.3, 128 12.3), and more in wide rows as long as a
+// thread's run stays eight steps in whole batches of four: the block's rows
+// lie closer together (GELU backward of 4097 x 8192: 128 threads 49 us, 32
+// 53, 256 50; of 8192 x 16384: 256 threads 159, 32 173).  A backward without
+// `wa` (`lean`) has a stream less to write and does better on one-warp rows
+// (16384 x 8192: 149 us, 160 with 128 threads), from 6 blocks an SM on (4097
+// x 8192: 64 threads 39, 32 43).  Of those the most that leave at most an
+// eighth of them idle in the row's last step (192 columns: 8 threads three
+// times, not 32 of which 8 idle).
 struct Shape { int lx, grid; };
-inline Shape shape(int rows, int cols) {
+inline Shape shape(int rows, int cols, bool lean = false) {
   const int vecs = cols / 8;
   int lx = 5;
-  while (lx < 8 && static_cast<long long>(rows) << lx < 6ll * 256 * num_sms()) ++lx;
+  while (lx < 8 && static_cast<long long>(rows) << lx < (lean ? 6ll : 3ll) * 256 * num_sms()) ++lx;
+  while (!lean && lx < 8 && vecs >= 16 << lx && vecs % (8 << lx) == 0) ++lx;
   for (; lx > 2; --lx) {
     const int tx = 1 << lx, padded = (vecs + tx - 1) / tx * tx;
     if ((padded - vecs) * 8 <= padded) break;
@@ -700,7 +707,7 @@ void run_backward(const int8_t* q, const uint8_t* e, const void* da, const float
   TD* hp = static_cast<TD*>(dh);
   TD* wp = static_cast<TD*>(wa);
   if (vec_ok(I, q, da, dh, wa)) {
-    const Shape p = shape(rows, I);
+    const Shape p = shape(rows, I, wa == nullptr);
     act_backward_vec_kernel<TS, TD, SW><<<p.grid, 256, 0, s>>>(q, e, dp, row_w, n_rows, rows, I, nb, p.lx, hp, wp, dw);
   } else {
     // one warp a row where that fills the GPU, else a block
