@@ -529,8 +529,9 @@ moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* 
  *          their outputs stay as they were;
  *   w      [G, N, K] in dtype (nn.Linear layout);
  *   sums   in fp32: on the tensor cores (whose adds truncate) at most 512
- *          terms at a time when the output is fp32, the parts added in fp32
- *          with rounding.  Fixed order: the same call gives the same bits.
+ *          terms at a time when the output is fp32 and 8192 when it is bf16,
+ *          the parts added in fp32 with rounding.  Fixed order: the same call
+ *          gives the same bits.
  * bf16 runs on the tensor cores when N and K are multiples of 8 (else on the
  * CUDA cores) and then needs x, dy, w, y, dx and dw on 16-byte boundaries
  * (MOE_ERR_INVALID_ARG otherwise); fp32 runs on the CUDA cores.  Tensors must

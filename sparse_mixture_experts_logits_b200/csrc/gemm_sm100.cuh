@@ -65,6 +65,8 @@ enum GemmEpilogue : int {
   EPI_GELU_KEEP = 15,
   EPI_KEPT_GELU_DACT = 16,
   EPI_KEPT_SWIGLU_DACT = 17,
+  // EPI_OUT_BF16 of contractions over kSwWholeBf16 terms, taken out that often
+  EPI_OUT_BF16_CHUNKED = 18,
 };
 
 // Operand layouts of the tokens-on-N GEMM (gemm_swap_sm100.cuh): the forward
@@ -75,6 +77,11 @@ enum SwapLayout : int { kSwFwd = 0, kSwDgrad = 1, kSwWgrad = 2, kSwWgradRagged =
 constexpr bool is_wgrad(int layout) { return layout == kSwWgrad || layout == kSwWgradRagged; }
 
 constexpr int kBK = 64;
+// Terms that a sum may have in the tensor cores' truncating fp32 adds: where
+// the output is fp32 (in k-blocks), and where it is rounded to bf16 (see
+// gemm_swap_sm100.cuh).
+constexpr int kSwChunk = 8;
+constexpr int kSwWholeBf16 = 8192;
 constexpr int kATileBytes = 128 * kBK * 2;  // 16 KB: 128 rows of A per CTA
 constexpr int kGemmThreads = 320;
 constexpr int kEpiWarps = 8;

@@ -126,6 +126,7 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     switch (epi) {
       case EPI_STORE_F32: return launch_swap_epi<EPI_STORE_F32, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16, kSwDgrad>(m, a, tiles_ub, s);
+      case EPI_OUT_BF16_CHUNKED: return launch_swap_epi<EPI_OUT_BF16_CHUNKED, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_KEPT_GELU_DACT: return launch_swap_epi<EPI_KEPT_GELU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_KEPT_SWIGLU_DACT: return launch_swap_epi<EPI_KEPT_SWIGLU_DACT, kSwDgrad>(m, a, tiles_ub, s);
       case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32, kSwDgrad>(m, a, tiles_ub, s);
@@ -146,6 +147,7 @@ cudaError_t launch_swap_rows(int layout, int epi, const SwapMaps& m, const SwapA
     case EPI_ACCUM_F32: return launch_swap_epi<EPI_ACCUM_F32>(m, a, tiles_ub, s);
     case EPI_OUT_F32: return launch_swap_epi<EPI_OUT_F32>(m, a, tiles_ub, s);
     case EPI_OUT_BF16: return launch_swap_epi<EPI_OUT_BF16>(m, a, tiles_ub, s);
+    case EPI_OUT_BF16_CHUNKED: return launch_swap_epi<EPI_OUT_BF16_CHUNKED>(m, a, tiles_ub, s);
     case EPI_SWIGLU_KEEP: return launch_swap_epi<EPI_SWIGLU_KEEP>(m, a, tiles_ub, s);
     case EPI_GELU_KEEP: return launch_swap_epi<EPI_GELU_KEEP>(m, a, tiles_ub, s);
   }

@@ -61,7 +61,14 @@
 // that are kept in fp32 (EPI_OUT_F32) are therefore summed in chunks of
 // kSwChunk k-blocks = 512 terms (5e-7): each chunk has a TMEM accumulator of
 // its own, and the epilogue warps add it, with rounding, to sums in their
-// registers while the next chunk's MMAs fill the other accumulator.
+// registers while the next chunk's MMAs fill the other accumulator.  Outputs
+// that are rounded to bf16 stay whole up to kSwWholeBf16 = 8192 terms
+// (EPI_OUT_BF16): the loss moves 0.1% of them to the neighbouring number at
+// 2048 terms and 0.4% at 8192, where chunks of 2048 would cost 2 to 5% of the
+// time and chunks of 512 up to 10% (64 experts x 256 rows x 8192 x 2048: 0.72
+// instead of 0.66 ms).  It grows with the length (2.8% of the value, seven
+// steps of bf16, at 2^22 positive terms), so longer sums are taken out every
+// 8192 terms (EPI_OUT_BF16_CHUNKED).
 #pragma once
 
 #include "ckpt.cuh"
@@ -73,7 +80,8 @@ namespace moe {
 // waits once and commits once per stage.  Two k-blocks per stage (3 stages
 // of 64 KB) measured faster than one (6 stages of 32 KB) and than three.
 constexpr int kSwKB = 2;
-constexpr int kSwChunk = 8;
+template <int EPI>
+constexpr int swap_chunk() { return EPI == EPI_OUT_BF16_CHUNKED ? kSwWholeBf16 / kBK : kSwChunk; }
 constexpr int kSwStages = 3;
 constexpr int kSwATileBytes = 128 * kBK * 2;  // 128 weight rows per CTA, one k-block
 constexpr int kSwBTileBytes = 128 * kBK * 2;  // up to 128 token rows per CTA, one k-block
@@ -290,6 +298,31 @@ __device__ __forceinline__ void swap_store(const SwapArgs& a, size_t base, int c
     static_cast<__nv_bfloat16*>(a.out)[base + row * a.ldo + col] = __float2bfloat16_rn(v);
 }
 
+// Stores 32 rows (v[i]: row `row` + i of this lane's column `col`, of which
+// `nv` exist; 0 where the column does not) in bf16.  Four rows at a time:
+// neighbouring lanes swap one shuffle's worth of halves, so that the even lane
+// holds both lanes' columns of rows 0 and 2 and the odd lane those of rows 1
+// and 3, and each 4-byte store covers two rows' 64-byte pieces (half the store
+// instructions of a column per lane; out_cols is even).
+__device__ __forceinline__ void store_bf16_rows32(const SwapArgs& a, const float (&v)[32], size_t row, int nv, int col,
+                                                  int lane) {
+  const bool odd = (lane & 1) != 0;
+  const size_t ld = a.ldo;
+  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + (row + (odd ? 1 : 0)) * ld + (col & ~1);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4, op += 4 * ld) {
+    const __nv_bfloat162 e = __floats2bfloat162_rn(v[i], v[i + 2]);
+    const __nv_bfloat162 o = __floats2bfloat162_rn(v[i + 1], v[i + 3]);
+    const uint32_t mine = odd ? *reinterpret_cast<const uint32_t*>(&o) : *reinterpret_cast<const uint32_t*>(&e);
+    const uint32_t give = odd ? *reinterpret_cast<const uint32_t*>(&e) : *reinterpret_cast<const uint32_t*>(&o);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+    const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;
+    const int rr = i + (odd ? 1 : 0);
+    if (rr < nv) *reinterpret_cast<uint32_t*>(op) = __byte_perm(lo, hi, 0x5410);
+    if (rr + 2 < nv) *reinterpret_cast<uint32_t*>(op + 2 * ld) = __byte_perm(lo, hi, 0x7632);
+  }
+}
+
 // GELU (tanh form) and its derivative from one tanh: with t = tanh u,
 // u = c (v + 0.044715 v^3) and s = 0.5 (1 + t), GELU(v) = v s and
 // GELU'(v) = s + 0.5 v (1 - t^2) c (1 + 3 * 0.044715 v^2).
@@ -396,7 +429,8 @@ template <int EPI, int LAYOUT>
 __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
     moe_gemm_swap_kernel(const __grid_constant__ SwapMaps maps, const SwapArgs args) {
   constexpr bool kWgrad = is_wgrad(LAYOUT);
-  constexpr bool kChunked = EPI == EPI_OUT_F32;
+  constexpr bool kChunked = EPI == EPI_OUT_F32 || EPI == EPI_OUT_BF16_CHUNKED;
+  constexpr int kChunk = swap_chunk<EPI>();
   constexpr int S = LAYOUT == kSwWgrad ? kSwWgStages : LAYOUT == kSwWgradRagged ? kSwRgStages : kSwStages;
   constexpr int KB = swap_kb<LAYOUT>();
   constexpr int kStage = swap_stage_bytes<LAYOUT>();
@@ -721,7 +755,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         for (int kb0 = 0; kb0 < t.nkb; kb0 += KB) {
           uint32_t kb_in = static_cast<uint32_t>(kb0);  // k-block inside its accumulator
           if constexpr (kChunked) {
-            kb_in = static_cast<uint32_t>(kb0 % kSwChunk);
+            kb_in = static_cast<uint32_t>(kb0 % kChunk);
             if (kb_in == 0) {
               if (kb0 != 0) {  // the chunk before is complete: hand it over, take the other accumulator
                 if (lane == 0) umma_commit_pair(smem_addr(&s_tfull[buf]), 0x3);
@@ -804,7 +838,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       const bool col_ok = col < args.out_cols;
       float bias = 0.f;
       if constexpr (EPI == EPI_GELU_BIAS || EPI == EPI_SCALE_BIAS || EPI == EPI_BIAS_ADD ||
-                    EPI == EPI_BWD_GELU_SAVE || EPI == EPI_GELU_KEEP || EPI == EPI_OUT_BF16 || (EPI == EPI_OUT_F32 && !kWgrad)) {
+                    EPI == EPI_BWD_GELU_SAVE || EPI == EPI_GELU_KEEP || EPI == EPI_OUT_BF16 || (kChunked && !kWgrad)) {
         if (args.bias != nullptr && col_ok)
           bias = __bfloat162float(args.bias[static_cast<size_t>(t.g) * args.out_cols + col]);
       }
@@ -836,7 +870,7 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
         for (int j = 0; j < kPieces; ++j)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
-        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSwChunk) {
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += kChunk) {
           if (kb0 != 0) ++it;
           const uint32_t cb = it & 1u;
           if (!mbar_wait_all(smem_addr(&s_tfull[cb]), (it >> 1) & 1u, abort_flag, args.status)) { ok = false; break; }
@@ -867,6 +901,12 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
           for (int j = 0; j < kPieces; ++j) {
             const int c = 32 * (part + kParts * j);
             const int nv = col_ok ? min(32, t.nrows - c) : 0;
+            if constexpr (EPI == EPI_OUT_BF16_CHUNKED) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[j][i] += bias;
+              store_bf16_rows32(args, sum[j], row0 + c, nv, col, lane);
+              continue;
+            }
             float* op = static_cast<float*>(args.out) + (row0 + c) * ld + col;
 #pragma unroll
             for (int i = 0; i < 32; ++i, op += ld)
@@ -952,30 +992,13 @@ __global__ void __launch_bounds__(swap_threads<EPI>(), 1)
       } else
       for (int c = 32 * part; c < t.n; c += 32 * kParts) {
         if constexpr (EPI == EPI_OUT_BF16) {
-          // Four rows at a time: neighbouring lanes swap one shuffle's worth
-          // of halves, so that the even lane holds both lanes' columns of rows
-          // 0 and 2 and the odd lane those of rows 1 and 3, and each 4-byte
-          // store covers two rows' 64-byte pieces (half the store
-          // instructions of a column per lane; out_cols is even).
           uint32_t r[32];
           MOE_TMEM_LD32(tacc + c, r);
           tmem_ld_wait();
-          const bool odd = (lane & 1) != 0;
-          const int nv = col_ok ? t.nrows - c : 0;
-          const size_t ld = args.ldo;
-          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(args.out) + (row0 + c + (odd ? 1 : 0)) * ld + (col & ~1);
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4, op += 4 * ld) {
-            const __nv_bfloat162 e = __floats2bfloat162_rn(__uint_as_float(r[i]) + bias, __uint_as_float(r[i + 2]) + bias);
-            const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(r[i + 1]) + bias, __uint_as_float(r[i + 3]) + bias);
-            const uint32_t mine = odd ? *reinterpret_cast<const uint32_t*>(&o) : *reinterpret_cast<const uint32_t*>(&e);
-            const uint32_t give = odd ? *reinterpret_cast<const uint32_t*>(&e) : *reinterpret_cast<const uint32_t*>(&o);
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;
-            const int rr = i + (odd ? 1 : 0);
-            if (rr < nv) *reinterpret_cast<uint32_t*>(op) = __byte_perm(lo, hi, 0x5410);
-            if (rr + 2 < nv) *reinterpret_cast<uint32_t*>(op + 2 * ld) = __byte_perm(lo, hi, 0x7632);
-          }
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) + bias;
+          store_bf16_rows32(args, v, row0 + c, col_ok ? t.nrows - c : 0, col, lane);
           continue;
         }
         // Every value this chunk reads from memory (the input-gradient

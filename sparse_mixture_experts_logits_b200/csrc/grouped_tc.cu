@@ -215,20 +215,19 @@ cudaError_t launch_grouped_tc(const GroupedLaunch& L, void* ws, cudaStream_t s) 
   }
   if (L.dir == kGroupedDgrad) {
     S.layout = kSwDgrad;
-    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;
     S.X = L.dy; S.x_rows = L.rows;
     S.K = L.N;
     S.a_cols = L.K;
     S.out_cols = L.K; S.ldo = L.K;
   } else {
     S.layout = kSwFwd;
-    S.epi = L.out_dtype == MOE_DTYPE_BF16 ? EPI_OUT_BF16 : EPI_OUT_F32;
     S.X = L.x; S.x_rows = L.rows;
     S.K = L.K;
     S.w_rows_per_group = L.N;
     S.out_cols = L.N; S.ldo = L.N;
     S.bias = L.bias;
   }
+  S.epi = L.out_dtype != MOE_DTYPE_BF16 ? EPI_OUT_F32 : S.K > kSwWholeBf16 ? EPI_OUT_BF16_CHUNKED : EPI_OUT_BF16;
   S.w_tiles = (S.out_cols + 255) / 256;
   return launch_gemm_swap(S, s);
 }
