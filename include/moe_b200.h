@@ -535,8 +535,8 @@ moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* 
  * bf16 runs on the tensor cores when N and K are multiples of 8 (else on the
  * CUDA cores) and then needs x, dy, w, y, dx and dw on 16-byte boundaries
  * (MOE_ERR_INVALID_ARG otherwise); fp32 runs on the CUDA cores.  Tensors must
- * not overlap.  Limits: G <= 1024, G N K < 2^40, rows < 2^30, N, K < 2^24.
- * rows = 0 is valid. */
+ * not overlap.  Limits: G <= 1024, G N K < 2^40, G N < 2^31 - 1024, rows <
+ * 2^30, N, K < 2^24.  rows = 0 is valid. */
 
 /* Workspace of moe_grouped_gemm and moe_grouped_dgrad; 0 if an argument is
  * invalid. */

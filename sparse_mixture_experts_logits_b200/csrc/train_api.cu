@@ -11,6 +11,9 @@ moe_status_t check_grouped(int G, int N, int K, int rows, int dtype) {
   if (!is_dtype(dtype) || G > kMaxExperts) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * K >= (1ll << 40) / G) return MOE_ERR_UNSUPPORTED;
   if (rows >= (1 << 30) || N >= (1 << 24) || K >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // The forward counts the weight rows of all experts in 32 bits, up to a tile behind the last one (its boxes'
+  // coordinates): past 2^31 they are no positions in the tensor, and loads at them faulted.
+  if (static_cast<long long>(G) * N >= (1ll << 31) - 1024) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
