@@ -89,9 +89,13 @@ class _Handle:
                 fn(*args)
 
     def _workspace(self, nbytes, stream):
-        """(256-byte aligned address, bytes, buffer); every call clears the status word itself"""
+        """(256-byte aligned address, bytes, buffer).  Every call with rows clears the status word itself; one without
+        leaves the workspace alone, so the word starts at 0."""
         buf = self._new((nbytes + 256,), torch.uint8, stream)
-        return buf.data_ptr() + (-buf.data_ptr()) % 256, nbytes, buf
+        off = (-buf.data_ptr()) % 256
+        with torch.cuda.stream(stream):
+            buf[off:off + 4].zero_()
+        return buf.data_ptr() + off, nbytes, buf
 
 
 class GroupedLinear(_Handle):

@@ -1,14 +1,13 @@
 """The grouped products and the checkpoints at the far ends of their documented
-ranges: long contractions, many weight rows, long segments, huge values, calls
-without rows (bounds as in train_ops_ref, derived beside each test where they
-are tighter)."""
+ranges: long contractions and segments, calls without rows (bounds as in
+train_ops_ref, derived beside each test where they are tighter)."""
 import numpy as np
 import pytest
 import torch
 
-import train_ops_ref as ref
-from gpu_common import np64
-from test_zzz_gpu_train_ops import _close, _dev, _offsets, _randn
+import moe_synth as ms
+from gpu_common import gpu_inputs, np64
+from test_zzz_gpu_train_ops import DT, _close, _dev, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +42,44 @@ def test_long_contractions_in_bf16(moe, direction, long):
         got = moe.GroupedLinear(w, 3).input_grad(x, _dev([0, 3]))
     bound = (3 * 512 * 2.0 ** -23 + (long / 8192 + 1) * 2.0 ** -24 + 2.0 ** -8) * np.abs(want)
     _close(got, want, bound, direction)
+
+
+def _poison(nbytes):
+    """Leaves blocks that are not zero for the allocator to give out again."""
+    junk = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (nbytes, nbytes + 256, 512, 1 << 20) for _ in range(8)]
+    torch.cuda.synchronize()
+    del junk
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_status_of_calls_without_rows(moe, dtype):
+    """Nothing ran, so nothing was reported."""
+    w = _randn(1, (3, 16, 24), DT[dtype])
+    x, dy = torch.empty(0, 24, dtype=DT[dtype], device="cuda"), torch.empty(0, 16, dtype=DT[dtype], device="cuda")
+    off, dt = _dev([0, 0, 0, 0]), moe.DTYPE_BF16 if dtype == "bf16" else moe.DTYPE_F32
+    _poison(moe.moe_grouped_workspace_size(3, 16, 24, 0, dt))
+    op = moe.GroupedLinear(w, 0)
+    op.forward(x, off)
+    assert op.device_status() == 0
+    op = moe.GroupedLinear(w, 0)
+    op.input_grad(dy, off)
+    assert op.device_status() == 0
+    _poison(moe.moe_grouped_wgrad_workspace_size(3, 16, 24, 0, dt))
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        op = moe.GroupedLinear(w, 0)
+        op.weight_grad(x, dy, off, stream=stream)
+        assert op.device_status(stream=stream) == 0
+
+
+@pytest.mark.parametrize("name", ["glm_small_bf16", "glam_tiny_f32"])
+def test_status_of_a_layer_without_tokens(moe, name):
+    cfg = ms.get_config(name)
+    inp = gpu_inputs(cfg)
+    layer = moe.MoELayer(cfg, inp, T=0)
+    ck, x = moe.LayerCheckpoint(layer), inp["x"][:0]
+    _poison(moe.moe_backward_saved_workspace_size(layer.desc))
+    _poison(moe.moe_forward_save_workspace_size(layer.desc))
+    layer.forward(x, checkpoint=ck)
+    layer.backward(x, x, checkpoint=ck)
+    assert layer.device_status() == 0 and layer.backward_status() == 0
