@@ -26,7 +26,9 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // db[g, n] (+)= sum over g's rows of dy[r, n] (N even).  A block of 256
 // threads takes share `z` of `shares` of group g's rows for the 64 columns of
 // column tile `nt`: its eight warps take every eighth row, two columns a
-// thread and eight rows in flight, and their sums are added in warp order.
+// thread and eight rows in flight, and their sums are added in warp order.  A
+// thread's sum goes to its total every 128 rows, so that a long segment's does
+// not lose the small ones.
 // With more than one share the blocks leave partial sums, which a second
 // kernel adds in order.  Bound by reading dy once.  `out`: group g's N sums
 // (or the share's partial ones); `s`: shared memory.
@@ -39,17 +41,23 @@ __device__ __forceinline__ void colsum_block(const __nv_bfloat16* __restrict__ d
   const int r0 = static_cast<int>(min(static_cast<long long>(e), b + static_cast<long long>(z) * per));
   const int r1 = min(e, r0 + per);
   const int n = nt * 64 + 2 * lane;
-  float2 a = make_float2(0.f, 0.f);
+  float2 a = make_float2(0.f, 0.f), tot = a;
   if (n < N) {
     const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(dy + static_cast<long long>(r0 + warp) * N + n);
     const long long step = 4ll * N;
-    int r = r0 + warp;
+    int r = r0 + warp, turns = 0;
     for (; r + 56 < r1; r += 64, p += 8 * step) {
       float2 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = __bfloat1622float2(p[i * step]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) { a.x += v[i].x; a.y += v[i].y; }
+      if (++turns == 16) {
+        turns = 0;
+        tot.x += a.x;
+        tot.y += a.y;
+        a = make_float2(0.f, 0.f);
+      }
     }
     for (; r < r1; r += 8, p += step) {
       const float2 v = __bfloat1622float2(*p);
@@ -58,7 +66,7 @@ __device__ __forceinline__ void colsum_block(const __nv_bfloat16* __restrict__ d
     }
   }
   __syncthreads();  // `s` of an earlier tile is read
-  s[warp][lane] = a;
+  s[warp][lane] = make_float2(tot.x + a.x, tot.y + a.y);
   __syncthreads();
   if (warp == 0 && n < N) {
     float2 v = s[0][lane];

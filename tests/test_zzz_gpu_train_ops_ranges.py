@@ -7,7 +7,7 @@ import torch
 
 import moe_synth as ms
 from gpu_common import gpu_inputs, np64
-from test_zzz_gpu_train_ops import DT, _close, _dev, _randn
+from test_zzz_gpu_train_ops import DT, _close, _dev, _offsets, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,23 @@ def test_status_of_a_layer_without_tokens(moe, name):
     layer.forward(x, checkpoint=ck)
     layer.backward(x, x, checkpoint=ck)
     assert layer.device_status() == 0 and layer.backward_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 1024])
+def test_bias_gradients_of_long_segments(moe, G, dtype):
+    """One large row and 10^5 small ones whose last bits the large one's sum does
+    not hold: at most 128 rounded additions in a row, and one for each 128 rows
+    behind them (added up in one order for all the segment's shares), not one
+    for each row.  1024 experts, all but one of them empty, are summed in one
+    share."""
+    rows, N, K = 100_000, 8, 8
+    counts = np.zeros(G, np.int64)
+    counts[G // 2] = rows
+    dy = torch.full((rows, N), 1.0078125, dtype=DT[dtype], device="cuda")
+    dy[0] = 2.0 ** 17
+    x, w = torch.zeros((rows, K), dtype=DT[dtype], device="cuda"), torch.zeros((G, N, K), dtype=DT[dtype], device="cuda")
+    db = moe.GroupedLinear(w, rows).weight_grad(x, dy, _dev(_offsets(counts)), db=True)[1]
+    want = np.zeros((G, N))
+    want[G // 2] = np64(dy).sum(0)
+    _close(db, want, (128 + rows / 128) * 2.0 ** -24 * np.abs(want), "db")
