@@ -511,7 +511,10 @@ moe_status_t moe_forward_save(const moe_layer_desc_t* d, const moe_weights_t* w,
 size_t moe_backward_saved_workspace_size(const moe_layer_desc_t* d);
 
 /* moe_backward from the checkpoint that moe_forward_save wrote for the same
- * descriptor, weights and x.  ckpt is only read.  Errors as moe_backward. */
+ * descriptor, weights and x.  ckpt is only read.  Errors as moe_backward.
+ * bf16: the weight gradients that run on the tensor cores are summed at most
+ * 512 terms at a time, as moe_grouped_wgrad's (moe_backward's sums stay whole
+ * there: 8e-4 of the value off for 2^17 positive terms). */
 moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x,
                                 const void* dy, const void* ckpt, size_t ckpt_bytes,
                                 const moe_grads_t* grads, void* ws, size_t ws_bytes, void* stream);

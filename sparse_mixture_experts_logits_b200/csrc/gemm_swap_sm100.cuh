@@ -61,8 +61,10 @@
 // that are kept in fp32 (EPI_OUT_F32) are therefore summed in chunks of
 // kSwChunk k-blocks = 512 terms (5e-7): each chunk has a TMEM accumulator of
 // its own, and the epilogue warps add it, with rounding, to sums in their
-// registers while the next chunk's MMAs fill the other accumulator.  Outputs
-// that are rounded to bf16 stay whole up to kSwWholeBf16 = 8192 terms
+// registers while the next chunk's MMAs fill the other accumulator.  (The
+// fp32 outputs of EPI_STORE_F32 stay whole: rows of an input gradient that are
+// rounded to bf16 behind it, and the recomputing backward's weight gradients.)
+// Outputs that are rounded to bf16 stay whole up to kSwWholeBf16 = 8192 terms
 // (EPI_OUT_BF16): the loss moves 0.1% of them to the neighbouring number at
 // 2048 terms and 0.4% at 8192, where chunks of 2048 would cost 2 to 5% of the
 // time and chunks of 512 up to 10% (64 experts x 256 rows x 8192 x 2048: 0.72

@@ -23,6 +23,12 @@ constexpr int kTail = kBK;     // rows of a group's tail buffer: one k-block
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// Rows [b, e) of group g; without offsets there is one group, of all rows.
+__device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, int g, int rows, int& b, int& e) {
+  b = offsets != nullptr ? max(0, min(offsets[g], rows)) : 0;
+  e = offsets != nullptr ? max(b, min(offsets[g + 1], rows)) : rows;
+}
+
 // db[g, n] (+)= sum over g's rows of dy[r, n] (N even).  A block of 256
 // threads takes share `z` of `shares` of group g's rows for the 64 columns of
 // column tile `nt`: its eight warps take every eighth row, two columns a
@@ -36,7 +42,8 @@ __device__ __forceinline__ void colsum_block(const __nv_bfloat16* __restrict__ d
                                              int rows, int N, int nt, int g, int z, int shares, int accumulate,
                                              float* __restrict__ out, float2 (*s)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = max(0, min(offsets[g], rows)), e = max(b, max(0, min(offsets[g + 1], rows)));
+  int b, e;
+  group_rows(offsets, g, rows, b, e);
   const int per = (e - b + shares - 1) / shares;
   const int r0 = static_cast<int>(min(static_cast<long long>(e), b + static_cast<long long>(z) * per));
   const int r1 = min(e, r0 + per);
@@ -130,7 +137,8 @@ __global__ void __launch_bounds__(256) wgrad_prepare_kernel(const uint4* __restr
                    db + static_cast<long long>(g) * 8 * vn, part);
     return;
   }
-  const int b = max(0, min(offsets[g], rows)), e = max(0, min(offsets[g + 1], rows));
+  int b, e;
+  group_rows(offsets, g, rows, b, e);
   const int tid = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   if (e <= b) {

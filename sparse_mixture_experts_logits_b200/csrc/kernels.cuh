@@ -118,7 +118,7 @@ struct GroupedLaunch {
   int dir;
   int dtype, out_dtype;
   int G, N, K, rows;
-  const int32_t* offsets;  // device [G + 1]
+  const int32_t* offsets;  // device [G + 1]; null (tensor-core weight gradients): one group of all rows
   const void* x;           // [rows, K]
   const void* dy;          // [rows, N]
   const void* w;

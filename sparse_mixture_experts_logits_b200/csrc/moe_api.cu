@@ -1191,12 +1191,26 @@ SwapLaunch bwd_swap(int epi, int layout, const void* A, long long a_rows, const 
   return L;
 }
 
+// out [N, K] = dy^T x over all T rows in chunked sums (bf16, workspace as for
+// launch_grouped_tc): the weight gradients of a backward from a checkpoint.
+cudaError_t token_weight_grad(const void* x, int K, const void* dy, int N, int T, float* out, void* wgrad, int* status,
+                              cudaStream_t s) {
+  GroupedLaunch L{};
+  L.dir = kGroupedWgrad;
+  L.dtype = MOE_DTYPE_BF16; L.out_dtype = MOE_DTYPE_F32;
+  L.G = 1; L.N = N; L.K = K; L.rows = T;
+  L.x = x; L.dy = dy; L.out = out;
+  L.status = status;
+  return launch_grouped_tc(L, wgrad, s);
+}
+
 // The shared expert's backward: its weight gradients, and its dx into dxs
 // (fp32).  The pre-activations are recomputed into hsb (fp32), or read from
-// the checkpoint (sq, se); asb gets a = act(h), dhsb dL/dh.
+// the checkpoint (sq, se; wgrad: the chunked weight gradients' workspace);
+// asb gets a = act(h), dhsb dL/dh.
 moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const void* dy,
-                                const moe_grads_t* g, void* hsb, int8_t* sq, uint8_t* se, void* asb, void* dhsb,
-                                float* dxs, int* status, cudaStream_t s) {
+                                const moe_grads_t* g, void* hsb, int8_t* sq, uint8_t* se, void* wgrad, void* asb,
+                                void* dhsb, float* dxs, int* status, cudaStream_t s) {
   const int T = d->T, D = d->D, Is = d->I_sh;
   const bool kept = sq != nullptr;
   if (Is > 0) {
@@ -1228,6 +1242,11 @@ moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* 
     SwapLaunch sc = bwd_swap(EPI_STORE_F32, kSwDgrad, w->sh_w1, 2ll * Is, dhsb, T, 2 * Is, 1, nullptr, nullptr, T,
                              D, dxs, D, status);
     MOE_CUDA(launch_gemm_swap(sc, s));
+    if (kept) {
+      MOE_CUDA(token_weight_grad(asb, Is, dy, D, T, g->dsh_w2, wgrad, status, s));
+      MOE_CUDA(token_weight_grad(x, D, dhsb, 2 * Is, T, g->dsh_w1, wgrad, status, s));
+      return MOE_OK;
+    }
     SwapLaunch sd = bwd_swap(EPI_STORE_F32, kSwWgrad, asb, T, dy, T, 0, 1, nullptr, nullptr, T, Is, g->dsh_w2, Is,
                              status);
     sd.b_cols = D;
@@ -1244,10 +1263,11 @@ moe_status_t shared_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* 
 
 // The router's backward: dW_r, and its dx added onto (or, without a shared
 // expert, written to) dxs.  dlb: bf16 dlogits when the two products run on the
-// tensor cores, else null and rpart holds the chunk sums of dW_r.
+// tensor cores, else null and rpart holds the chunk sums of dW_r.  wgrad (from
+// a checkpoint, else null): dW_r in chunked sums, and their workspace.
 moe_status_t router_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x, const float* logits,
                                 const int32_t* idx, const float* dwp, float* dl, void* dlb, float* dxs, float* rpart,
-                                const moe_grads_t* g, int* status, cudaStream_t s) {
+                                void* wgrad, const moe_grads_t* g, int* status, cudaStream_t s) {
   const int T = d->T, D = d->D, M = d->M, k = d->k, Is = d->I_sh;
   {
     Range r("moe.router_backward");
@@ -1257,12 +1277,16 @@ moe_status_t router_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* 
     if (tc) {
       // dW_r [D, M] = x^T dlogits: the weight-gradient layout over one group of T rows,
       // dlogits (bf16) on the A side so that its M columns are the output's contiguous ones
-      SwapLaunch gw = bwd_swap(EPI_STORE_F32, kSwWgrad, dlb, T, x, T, 0, 1, nullptr, nullptr, T, M, g->dw_r, M,
-                               status);
-      gw.b_cols = D;
-      gw.b_tiles = (D + 255) / 256;
-      gw.out_gstride = 1ll * D * M;
-      MOE_CUDA(launch_gemm_swap(gw, s));
+      if (wgrad != nullptr) {
+        MOE_CUDA(token_weight_grad(dlb, M, x, D, T, g->dw_r, wgrad, status, s));
+      } else {
+        SwapLaunch gw = bwd_swap(EPI_STORE_F32, kSwWgrad, dlb, T, x, T, 0, 1, nullptr, nullptr, T, M, g->dw_r, M,
+                                 status);
+        gw.b_cols = D;
+        gw.b_tiles = (D + 255) / 256;
+        gw.out_gstride = 1ll * D * M;
+        MOE_CUDA(launch_gemm_swap(gw, s));
+      }
       // dx += dlogits W_r^T: the forward layout, W_r [D, M] as K-major weight rows (K = M),
       // added onto the shared expert's dx when there is one
       SwapLaunch gx = bwd_swap(Is > 0 ? EPI_ACCUM_F32 : EPI_STORE_F32, kSwFwd, w->w_r, D, dlb, T, M, 1, nullptr,
@@ -1319,8 +1343,10 @@ SavedWs saved_layout(const moe_layer_desc_t* d) {
     L.dhs = c.take(T * 2 * Is * 2);
     L.rpart = router_bwd_tc(d) ? 0 : c.take(static_cast<size_t>(router_ksplit(d->T)) * D * M * 4);
     L.dlb = router_bwd_tc(d) ? c.take(T * M * 2) : 0;
-    L.wgrad = c.take(std::max(grouped_tc_workspace(kGroupedWgrad, d->M, d->D, d->I),
-                              grouped_tc_workspace(kGroupedWgrad, d->M, static_cast<int>(n1), d->D)));
+    L.wgrad = c.take(std::max({grouped_tc_workspace(kGroupedWgrad, d->M, d->D, d->I),
+                               grouped_tc_workspace(kGroupedWgrad, d->M, static_cast<int>(n1), d->D),
+                               grouped_tc_workspace(kGroupedWgrad, 1, 2 * d->I_sh, d->D),
+                               grouped_tc_workspace(kGroupedWgrad, 1, d->D, d->M)}));
     const int shares = grouped_colsum_shares(d->M, static_cast<int>(pairs), d->I);
     L.colsum = c.take(shares > 1 ? static_cast<size_t>(shares) * M * Ha * 4 : 0);
   } else {
@@ -1421,10 +1447,11 @@ moe_status_t saved_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w
   }
   if (d->I_sh > 0)
     MOE_TRY(shared_backward_tc(d, w, x, dy, g, nullptr, at<int8_t*>(ckpt, C.sq), at<uint8_t*>(ckpt, C.se),
-                               at<void*>(ws, L.as), at<void*>(ws, L.dhs), dxs, status, s));
+                               at<void*>(ws, L.wgrad), at<void*>(ws, L.as), at<void*>(ws, L.dhs), dxs, status, s));
   MOE_TRY(router_backward_tc(d, w, x, logits, idx, dwp, at<float*>(ws, L.dl),
                              router_bwd_tc(d) ? at<void*>(ws, L.dlb) : nullptr, dxs,
-                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), g, status, s));
+                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), at<void*>(ws, L.wgrad), g, status,
+                             s));
   {
     Range r("moe.combine_backward");
     MOE_CUDA(launch_combine(d->dtype, dxp, slot_of, dxs, true, nullptr, g->dx, T, D, k, s));
@@ -1555,10 +1582,10 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
       MOE_CUDA(launch_colsum_bf16(dhb, n1, nullptr, offp, M, P, Ha, g->db1, s));
     }
   }
-  MOE_TRY(shared_backward_tc(d, w, x, dy, g, at<void*>(ws, L.hsb), nullptr, nullptr, at<void*>(ws, L.asb),
-                             at<void*>(ws, L.dhsb), dxs, status, s));
+  MOE_TRY(shared_backward_tc(d, w, x, dy, g, at<void*>(ws, L.hsb), nullptr, nullptr, nullptr,
+                             at<void*>(ws, L.asb), at<void*>(ws, L.dhsb), dxs, status, s));
   MOE_TRY(router_backward_tc(d, w, x, logits, idx, dwp, dl, router_bwd_tc(d) ? at<void*>(ws, L.dlb) : nullptr, dxs,
-                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), g, status, s));
+                             router_bwd_tc(d) ? nullptr : at<float*>(ws, L.rpart), nullptr, g, status, s));
   {
     Range r("moe.combine_backward");
     MOE_CUDA(launch_combine(d->dtype, dxpp, slotp, dxs, true, nullptr, g->dx, T, D, k, s));

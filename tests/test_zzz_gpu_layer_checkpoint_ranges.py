@@ -1,0 +1,70 @@
+"""The layer with a checkpoint at the far ends of its range: many tokens."""
+import pytest
+import torch
+
+import moe_synth as ms
+from gpu_common import gpu_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    import sparse_mixture_experts_logits_b200 as B
+    return B
+
+
+def _uniform(seed, shape, lo, hi, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, device="cuda", generator=g) * (hi - lo) + lo).to(dtype)
+
+
+def _kept(ck, name):
+    """The kept values of SwiGLU pre-activations: (gate, up) in 64 bits (one block of at most 32 columns a half)."""
+    q, e = ck.view(name + "q").double(), ck.view(name + "e").long()
+    c = q.shape[1] // 2
+    step = (e - 133 + 1023 << 52).view(torch.float64)
+    return q[:, :c] * step[:, :1], q[:, c:] * step[:, 1:]
+
+
+def _close(got, want, rel, what):
+    off = float(((got.double() - want).abs() / want.abs()).max())
+    assert off <= rel, f"{what}: {off:.3g} of the value, bound {rel:.3g}"
+
+
+def test_gradients_over_many_tokens(B):
+    """The weight gradients that sum over every token (the shared expert's and
+    the router's) are off by the roundings of 512 terms at a time, and not by how
+    many tokens there are.
+
+    All terms are positive, so that a truncated addition's loss adds up.  Bound:
+    32 truncated steps of 16 products (3 * 2^-23 each), one rounded addition for
+    each 512 terms, and 2^-17 for the operands: they are rounded to bf16 from
+    fp32 values a few 2^-21 off the reference's, which moves some of them to the
+    neighbouring number, by 2^-21 of the sum on average."""
+    T, I = 1 << 17, 16
+    cfg = ms.get_config("glm_small_bf16", T=T, D=64, M=64, k=1, I=I, I_sh=I, norm_topk_prob=0, alpha=1.0)
+    t = dict(gpu_inputs(dict(cfg, T=16)), x=_uniform(1, (T, 64), 0.5, 1.0), w_r=_uniform(2, (64, 64), 0.0, 0.02),
+             w1=_uniform(3, (64, 2 * I, 64), 0.0, 0.05), w2=_uniform(4, (64, 64, I), 0.5, 1.0),
+             sh_w1=_uniform(5, (2 * I, 64), 0.0, 0.05), sh_w2=_uniform(6, (64, I), 0.5, 1.0))
+    t["e_bias"] = torch.zeros_like(t["e_bias"])
+    t["e_bias"][0] = 100.0  # every token goes to expert 0, so that dispatch order is the tokens'
+    x, dy = t["x"], _uniform(7, (T, 64), 1.0, 2.0)
+    layer = B.MoELayer(cfg, t)
+    ck = B.LayerCheckpoint(layer)
+    layer.forward(x, checkpoint=ck)
+    got = layer.backward(x, dy, checkpoint=ck)
+    assert layer.backward_status() == 0 and not ck.view("topk_idx").any()
+    bf = lambda v: v.to(torch.bfloat16).double()  # noqa: E731
+    x, dy = x.double(), dy.double()
+    g, u = _kept(ck, "shared_")
+    s, G = torch.sigmoid(g), dy @ t["sh_w2"].double()
+    dh = torch.cat([G * u * s * (1 + g * (1 - s)), G * g * s], 1)
+    bound = 3 * 32 * 2.0 ** -23 + (T / 512 + 1) * 2.0 ** -24 + 2.0 ** -17
+    _close(got["dsh_w2"], dy.T @ bf(g * s * u), bound, "dsh_w2")
+    _close(got["dsh_w1"], bf(dh).T @ x, bound, "dsh_w1")
+    g, u = _kept(ck, "")
+    dw = (dy @ t["w2"][0].double() * g * torch.sigmoid(g) * u).sum(1)
+    p = torch.sigmoid(ck.view("logits")[:, 0].double())
+    _close(got["dw_r"][:, 0], x.T @ bf(dw * p * (1 - p)), bound, "dw_r")
+    assert not got["dw_r"][:, 1:].any()
