@@ -184,7 +184,9 @@ __device__ __forceinline__ float gelu_tanh_grad(float v) {
   // d/dv of 0.5 v (1 + tanh u), u = c (v + 0.044715 v^3)
   const float c = 0.7978845608028654f;
   const float th = tanhf(c * (v + 0.044715f * v * v * v));
-  return 0.5f * (1.0f + th) + 0.5f * v * (1.0f - th * th) * c * (1.0f + 3.0f * 0.044715f * v * v);
+  // kept finite where v^2 overflows: 1 - th^2 is 0 long before
+  const float vc = fmaxf(fminf(v, 1e9f), -1e9f);
+  return 0.5f * (1.0f + th) + 0.5f * v * (1.0f - th * th) * c * (1.0f + 3.0f * 0.044715f * vc * vc);
 }
 
 // In place: h (pre-activations) becomes dL/dh, from da = dL/da.  The thread of

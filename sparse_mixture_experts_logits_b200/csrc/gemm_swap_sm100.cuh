@@ -327,14 +327,15 @@ __device__ __forceinline__ void store_bf16_rows32(const SwapArgs& a, const float
 
 // GELU (tanh form) and its derivative from one tanh: with t = tanh u,
 // u = c (v + 0.044715 v^3) and s = 0.5 (1 + t), GELU(v) = v s and
-// GELU'(v) = s + 0.5 v (1 - t^2) c (1 + 3 * 0.044715 v^2).
+// GELU'(v) = s + 0.5 v (1 - t^2) c (1 + 3 * 0.044715 v^2).  The last factor's
+// square is kept finite where v^2 overflows: 1 - t^2 is 0 long before.
 __device__ __forceinline__ void gelu_tanh_and_grad_fast(float v, float& g, float& dg) {
   const float c = 0.7978845608028654f;
   const float u = c * fmaf(0.044715f * v, v * v, v);
   const float t = tanh_hw(u);
   const float s = fmaf(0.5f, t, 0.5f);  // 0.5 (1 + tanh u)
   g = v * s;
-  dg = fmaf(0.5f * v * fmaf(-t, t, 1.0f) * c, fmaf(3.0f * 0.044715f, v * v, 1.0f), s);
+  dg = fmaf(0.5f * v * fmaf(-t, t, 1.0f) * c, fmaf(3.0f * 0.044715f, fminf(v * v, 1e18f), 1.0f), s);
 }
 
 // Sum over the warp's 32 lanes of v[i] for every i, in 31 shuffles: after

@@ -1,4 +1,5 @@
-"""The layer with a checkpoint at the far ends of its range: many tokens."""
+"""The layer with a checkpoint at the far ends of its range: many tokens, huge
+pre-activations."""
 import pytest
 import torch
 
@@ -68,3 +69,26 @@ def test_gradients_over_many_tokens(B):
     p = torch.sigmoid(ck.view("logits")[:, 0].double())
     _close(got["dw_r"][:, 0], x.T @ bf(dw * p * (1 - p)), bound, "dw_r")
     assert not got["dw_r"][:, 1:].any()
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("name", ["glam_small_bf16", "glam_nonorm_f32"])
+def test_huge_gelu_pre_activations(B, name, saved):
+    """Scaling the up projection by 2^27 where every pre-activation is already far
+    out on GELU's straight pieces scales some gradients by 2^27 and leaves the
+    others, bit for bit; the squares of the larger ones are no fp32 numbers."""
+    cfg = ms.get_config(name)
+    inp = gpu_inputs(cfg)
+    inp["b2"].zero_()
+    dy = ms.upstream_grad(cfg, "cuda")
+    got = []
+    for p in (40, 67):
+        t = dict(inp, w1=inp["w1"] * 2.0 ** p, b1=inp["b1"] * 2.0 ** p)
+        layer = B.MoELayer(cfg, t)
+        ck = B.LayerCheckpoint(layer) if saved else None
+        y = layer.forward(t["x"], checkpoint=ck)
+        got.append(dict(layer.backward(t["x"], dy, checkpoint=ck), y=y))
+    for n, small in got[0].items():
+        scale = 1.0 if n in ("dw1", "db1", "db2") else 2.0 ** 27
+        assert got[1][n].isfinite().all(), n
+        assert torch.equal(got[1][n], small * scale), n
