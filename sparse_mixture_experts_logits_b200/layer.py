@@ -147,11 +147,12 @@ class MoELayer:
 
     def _scratch(self, nbytes: int, stream):
         """(buffer, offset of its first 256-byte boundary, bytes), allocated on the stream that will use it.  Its first
-        word is the status, which a call without tokens leaves as it is."""
+        word is the status, which every call with tokens clears and one without leaves as it is."""
         with torch.cuda.stream(stream):
             buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
             off = (-buf.data_ptr()) % 256
-            buf[off:off + 4].zero_()
+            if self.desc.T == 0:
+                buf[off:off + 4].zero_()
         return buf, off, nbytes
 
     def device_status(self, stream=None) -> int:

@@ -40,6 +40,7 @@ class _Handle:
     """The device, and the checks of every tensor against it."""
 
     device: torch.device
+    rows: int
 
     def _in(self, name, t, shape, dtype):
         """t's address; t must be a contiguous [shape] tensor of dtype on the handle's device."""
@@ -89,12 +90,13 @@ class _Handle:
                 fn(*args)
 
     def _workspace(self, nbytes, stream):
-        """(256-byte aligned address, bytes, buffer).  Every call with rows clears the status word itself; one without
-        leaves the workspace alone, so the word starts at 0."""
+        """(256-byte aligned address, bytes, buffer).  Every call with rows clears the status word itself; without rows
+        no call touches the workspace, so that the word has to start at 0."""
         buf = self._new((nbytes + 256,), torch.uint8, stream)
         off = (-buf.data_ptr()) % 256
-        with torch.cuda.stream(stream):
-            buf[off:off + 4].zero_()
+        if self.rows == 0:
+            with torch.cuda.stream(stream):
+                buf[off:off + 4].zero_()
         return buf.data_ptr() + off, nbytes, buf
 
 
