@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import moe_synth as ms
+import train_ops_ref as ref
 from gpu_common import gpu_inputs, np64
 from test_zzz_gpu_train_ops import DT, _close, _dev, _offsets, _randn
 
@@ -103,3 +104,45 @@ def test_bias_gradients_of_long_segments(moe, G, dtype):
     want = np.zeros((G, N))
     want[G // 2] = np64(dy).sum(0)
     _close(db, want, (128 + rows / 128) * 2.0 ** -24 * np.abs(want), "db")
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+def test_several_chunks_and_several_tiles(moe, dtype, out):
+    """Accumulators taken out one to three times a tile, and several tiles for
+    each pair of processors: what a tile leaves (the accumulator that is next,
+    the store buffers, the prefetch a tile ahead) is carried to the next one."""
+    counts = [600, 1100, 0, 64, 1, 513] if dtype == "bf16" else [600, 0, 65]
+    offsets, N, K = _offsets(counts), 1032, 1544
+    rows, G = int(offsets[-1]), len(counts)
+    x, dy, w = _randn(1, (rows, K), DT[dtype]), _randn(2, (rows, N), DT[dtype]), _randn(3, (G, N, K), DT[dtype], K ** -0.5)
+    off, op = _dev(offsets), moe.GroupedLinear(w, rows, out_dtype=DT[out])
+    hx, hdy, hw = np64(x), np64(dy), np64(w)
+    want, m = ref.grouped_gemm(hx, hw, None, offsets, np.zeros((rows, N)))
+    _close(op.forward(x, off), want, ref.gamma(K, out) * m + ref.U[out] * np.abs(want), "y")
+    want, m = ref.grouped_dgrad(hdy, hw, offsets, np.zeros((rows, K)))
+    _close(op.input_grad(dy, off), want, ref.gamma(N, out) * m + ref.U[out] * np.abs(want), "dx")
+    dw0, db0 = _randn(5, (G, N, K), torch.float32), _randn(6, (G, N), torch.float32)
+    for add in (False, True):
+        base = (np64(dw0), np64(db0)) if add else (None, None)
+        ww, wb, mw, mb = ref.grouped_wgrad(hx, hdy, offsets, *base)
+        dw, db = op.weight_grad(x, dy, off, dw=dw0.clone(), db=db0.clone(), accumulate=add)
+        _close(dw, ww, (ref.gamma(max(counts), "f32") + 2.0 ** -24) * mw, "dw")
+        _close(db, wb, (128 + max(counts) / 128 + 9) * 2.0 ** -24 * mb, "db")
+    assert op.device_status() == 0
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_chunks_of_claimed_tiles(moe, out):
+    """Many narrow experts and a long one: the pairs of processors claim their
+    tiles from the counter, with two and three accumulators a tile."""
+    counts = [1 + 13 * g % 40 for g in range(60)] + [700]
+    offsets, N, K = _offsets(counts), 1288, 584   # 21 and 10 blocks of 64 terms
+    rows, G = int(offsets[-1]), len(counts)
+    x, dy, w = _randn(1, (rows, K), torch.bfloat16), _randn(2, (rows, N), torch.bfloat16), _randn(3, (G, N, K), torch.bfloat16, K ** -0.5)
+    off, op = _dev(offsets), moe.GroupedLinear(w, rows, out_dtype=DT[out])
+    for _ in range(3):
+        want, m = ref.grouped_gemm(np64(x), np64(w), None, offsets, np.zeros((rows, N)))
+        _close(op.forward(x, off), want, ref.gamma(K, out) * m + ref.U[out] * np.abs(want), "y")
+        want, m = ref.grouped_dgrad(np64(dy), np64(w), offsets, np.zeros((rows, K)))
+        _close(op.input_grad(dy, off), want, ref.gamma(N, out) * m + ref.U[out] * np.abs(want), "dx")
+    assert op.device_status() == 0
