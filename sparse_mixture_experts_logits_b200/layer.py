@@ -122,9 +122,11 @@ class MoELayer:
                 addend: torch.Tensor | None = None, checkpoint: LayerCheckpoint | None = None) -> torch.Tensor:
         """y = MoE-FFN(x), or addend + MoE-FFN(x) when ``addend`` is given.
         With ``checkpoint`` the pass also keeps there what
-        ``backward(..., checkpoint=...)`` needs (moe_forward_save)."""
+        ``backward(..., checkpoint=...)`` needs (moe_forward_save).  What a
+        call allocates is allocated on the stream that it runs on."""
         if y is None:
-            y = torch.empty_like(x)
+            with torch.cuda.stream(stream):
+                y = torch.empty_like(x)
         if checkpoint is not None:
             if self._save is None:
                 nbytes = abi.moe_forward_save_workspace_size(self.desc)
@@ -184,14 +186,16 @@ class MoELayer:
             self.bws_bytes = abi.moe_backward_workspace_size(self.desc)
             if self.bws_bytes == 0:
                 raise abi.MoEError("moe_backward_workspace_size", abi.MOE_ERR_INVALID_ARG)
-            self._bws = torch.zeros(self.bws_bytes + 256, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(stream):
+                self._bws = torch.zeros(self.bws_bytes + 256, dtype=torch.uint8, device=self.device)
             self._bws_off = (-self._bws.data_ptr()) % 256
         if grads is None:
             grads = {}
-            for name, shape in self.grad_shapes().items():
-                if shape is not None:
-                    dt = x.dtype if name == "dx" else torch.float32
-                    grads[name] = torch.empty(shape, dtype=dt, device=self.device)
+            with torch.cuda.stream(stream):
+                for name, shape in self.grad_shapes().items():
+                    if shape is not None:
+                        dt = x.dtype if name == "dx" else torch.float32
+                        grads[name] = torch.empty(shape, dtype=dt, device=self.device)
         g = abi.Grads()
         for name in abi.Grads._fields_:
             setattr(g, name[0], _ptr(grads.get(name[0])))
@@ -268,7 +272,8 @@ class DenseLayer:
                 stream=None) -> torch.Tensor:
         """y = (addend +) FFN(x)."""
         if y is None:
-            y = torch.empty_like(x)
+            with torch.cuda.stream(stream):
+                y = torch.empty_like(x)
         abi.moe_dense_ffn(self.desc, *self.args(), x.data_ptr(), _ptr(addend), y.data_ptr(), self.ws_ptr,
                           self.ws_bytes, _stream_handle(stream))
         return y

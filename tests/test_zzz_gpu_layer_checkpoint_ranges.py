@@ -92,3 +92,34 @@ def test_huge_gelu_pre_activations(B, name, saved):
         scale = 1.0 if n in ("dw1", "db1", "db2") else 2.0 ** 27
         assert got[1][n].isfinite().all(), n
         assert torch.equal(got[1][n], small * scale), n
+
+
+@pytest.mark.parametrize("name,kept", [("glm_small_bf16", True), ("glm_small_bf16", False), ("glm_small_f32", True)])
+def test_a_stream_of_its_own(B, name, kept):
+    """A call on a given stream while the current one is busy: what it allocates
+    is not written by work that is still to run on the current stream."""
+    cfg = ms.get_config(name)
+    inp = gpu_inputs(cfg)
+    x, dy, h = inp["x"], ms.upstream_grad(cfg, "cuda"), inp["x"].clone()
+    layer = B.MoELayer(cfg, inp)
+    ck = B.LayerCheckpoint(layer) if kept else None
+    y0 = layer.forward(x, addend=h, checkpoint=ck)
+    want = layer.backward(x, dy, checkpoint=ck)
+    layer = B.MoELayer(cfg, inp)
+    ck = B.LayerCheckpoint(layer) if kept else None
+    side, busy = torch.cuda.Stream(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(100):
+        busy.fill_(1)
+    # blocks of the results' sizes that the current stream will still write, after a while
+    sizes = [y0] + list(want.values())
+    junk = [torch.full_like(t, float("nan")) for t in sizes for _ in range(2)]
+    junk.append(torch.full((1 << 26,), 0x7F, dtype=torch.uint8, device="cuda"))
+    del junk
+    y = layer.forward(x, addend=h, checkpoint=ck, stream=side)
+    got = layer.backward(x, dy, checkpoint=ck, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y0)
+    for n, v in want.items():
+        assert torch.equal(got[n], v), n
+    assert layer.device_status(stream=side) == 0 and layer.backward_status(stream=side) == 0
