@@ -29,6 +29,13 @@ def _dtype(dt):
         raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, not {dt}") from None
 
 
+def _int32(name, v):
+    """v, which the C interface takes in 32 bits."""
+    if not -2 ** 31 <= int(v) < 2 ** 31:
+        raise ValueError(f"{name} = {v} is no 32-bit number")
+    return int(v)
+
+
 def _device(device):
     d = torch.device(device)
     if d.type != "cuda":
@@ -118,9 +125,9 @@ class GroupedLinear(_Handle):
         if weight.dim() != 3:
             raise ValueError("weight must be [G, N, K]")
         self.device = _device(weight.device)
-        self.dtype, self.rows = weight.dtype, int(rows)
+        self.dtype, self.rows = weight.dtype, _int32("rows", rows)
         self.out_dtype = weight.dtype if out_dtype is None else out_dtype
-        self.G, self.N, self.K = weight.shape
+        self.G, self.N, self.K = (_int32("a dimension of weight", d) for d in weight.shape)
         self._dt, self._odt = _dtype(self.dtype), _dtype(self.out_dtype)
         self._in("weight", weight, (self.G, self.N, self.K), self.dtype)
         self._opt("bias", bias, (self.G, self.N), self.dtype)
@@ -187,7 +194,7 @@ class RowCheckpoint(_Handle):
 
     def __init__(self, rows: int, cols: int, dtype: torch.dtype, device="cuda"):
         self.device = _device(device)
-        self.rows, self.cols, self.dtype = int(rows), int(cols), dtype
+        self.rows, self.cols, self.dtype = _int32("rows", rows), _int32("cols", cols), dtype
         self._dt = _dtype(dtype)
         self.blocks = abi.moe_ckpt_blocks(self.cols)
         if self.rows < 0 or self.blocks == 0:
@@ -206,7 +213,7 @@ class RowCheckpoint(_Handle):
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The kept rows, or rows row_index[r] of them (int32; an index out of
         range gives a zero row and sets ``status``)."""
-        n = self.rows if row_index is None else row_index.numel()
+        n = self.rows if row_index is None else _int32("rows of row_index", row_index.numel())
         pi = self._opt("row_index", row_index, (n,), torch.int32)
         out = self._out("out", out, (n, self.cols), self.dtype, stream)
         self._call(abi.moe_ckpt_dequantize, self.q.data_ptr(), self.e.data_ptr(), pi,
@@ -228,7 +235,7 @@ class ActivationCheckpoint(_Handle):
         if act not in _ACTS:
             raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}")
         self.device = _device(device)
-        self.act, self.rows, self.I, self.dtype = act, int(rows), int(I), dtype
+        self.act, self.rows, self.I, self.dtype = act, _int32("rows", rows), _int32("I", I), dtype
         self.src_dtype = dtype if src_dtype is None else src_dtype
         self._dts = (_ACTS[act], _dtype(dtype), _dtype(self.src_dtype))
         halves = 2 if act == "swiglu" else 1
@@ -252,7 +259,7 @@ class ActivationCheckpoint(_Handle):
     def load(self, stream=None) -> torch.Tensor:
         """The kept h [rows, width], in dtype."""
         out = self._new((self.rows, self.width), self.dtype, stream)
-        n = self.rows * self._halves
+        n = _int32("rows", self.rows * self._halves)
         self._call(abi.moe_ckpt_dequantize, self.q.data_ptr(), self.e.data_ptr(), None, None, n, n, self.I,
                    self._dts[1], out.data_ptr(), None, self._stream(stream))
         return out

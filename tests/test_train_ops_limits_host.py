@@ -1,6 +1,7 @@
 """Limits of the grouped products: calls past them are answered on the host,
 before anything is launched (no GPU needed)."""
 import pytest
+import torch
 
 from test_train_ops_host import _dgrad, _gemm, _status, _wgrad, moe  # noqa: F401
 
@@ -18,3 +19,14 @@ def test_weight_rows_that_32_bits_do_not_count(moe, G, N, K, dtype):  # noqa: F8
     for fn in (moe.moe_grouped_workspace_size, moe.moe_grouped_wgrad_workspace_size):
         assert fn(G, N, K, 10, dtype) == 0
         assert fn(1024, (1 << 21) - 8, K, 10, dtype) > 0  # the largest that is open
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 4, -(1 << 31) - 1])
+def test_sizes_that_32_bits_do_not_hold(moe, n):  # noqa: F811
+    """The C interface takes sizes in 32 bits: a larger one is refused, not cut off to its low bits."""
+    for make in (lambda: moe.RowCheckpoint(n, 8, torch.bfloat16, device="cuda:0"),
+                 lambda: moe.RowCheckpoint(8, n, torch.bfloat16, device="cuda:0"),
+                 lambda: moe.ActivationCheckpoint("swiglu", n, 8, torch.bfloat16, device="cuda:0"),
+                 lambda: moe.ActivationCheckpoint("gelu_tanh", 8, n, torch.bfloat16, device="cuda:0")):
+        with pytest.raises(ValueError, match="32-bit"):
+            make()

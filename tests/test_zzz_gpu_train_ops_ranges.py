@@ -146,3 +146,9 @@ def test_chunks_of_claimed_tiles(moe, out):
         want, m = ref.grouped_dgrad(np64(dy), np64(w), offsets, np.zeros((rows, K)))
         _close(op.input_grad(dy, off), want, ref.gamma(N, out) * m + ref.U[out] * np.abs(want), "dx")
     assert op.device_status() == 0
+
+
+@pytest.mark.parametrize("rows", [1 << 31, (1 << 32) + 4])
+def test_rows_that_32_bits_do_not_hold(moe, rows):
+    with pytest.raises(ValueError, match="32-bit"):
+        moe.GroupedLinear(_randn(1, (2, 16, 24), torch.bfloat16), rows)
