@@ -148,6 +148,33 @@ def test_chunks_of_claimed_tiles(moe, out):
     assert op.device_status() == 0
 
 
+@pytest.mark.parametrize("direction", ["forward", "input_grad"])
+@pytest.mark.parametrize("counts", [[64 + g % 5 for g in range(40)], [1 + 13 * g % 40 for g in range(40)], [600]])
+def test_long_contractions_over_several_tiles(moe, counts, direction):
+    """bf16 outputs of three accumulators a tile and several tiles a pair of
+    processors, in fixed rounds and claimed, the last block of the sum a partial one."""
+    G, width, long = len(counts), 264, 2 * 8192 + 72
+    offsets = _offsets(counts)
+    rows = int(offsets[-1])
+    forward = direction == "forward"
+    x = _randn(1, (rows, long), torch.bfloat16)
+    w = _randn(2, (G, width, long) if forward else (G, long, width), torch.bfloat16, long ** -0.5)
+    bias = _randn(3, (G, width), torch.bfloat16) if forward else None
+    op = moe.GroupedLinear(w, rows, bias=bias)
+    for _ in range(2):
+        got = op.forward(x, _dev(offsets)) if forward else op.input_grad(x, _dev(offsets))
+        for g in range(G):
+            r = slice(int(offsets[g]), int(offsets[g + 1]))
+            a, b = x[r].double(), w[g].double().T if forward else w[g].double()
+            want, m = a @ b, a.abs() @ b.abs()
+            if forward:
+                want, m = want + bias[g].double(), m + bias[g].double().abs()
+            # as ref.gamma of 8192 terms, one rounded addition for each such part, and the rounding to bf16
+            bound = (ref.gamma(8192, "bf16") + 4 * 2.0 ** -24) * m + ref.U["bf16"] * want.abs()
+            assert bool(((got[r].double() - want).abs() <= bound).all()), g
+    assert op.device_status() == 0
+
+
 @pytest.mark.parametrize("rows", [1 << 31, (1 << 32) + 4])
 def test_rows_that_32_bits_do_not_hold(moe, rows):
     with pytest.raises(ValueError, match="32-bit"):
