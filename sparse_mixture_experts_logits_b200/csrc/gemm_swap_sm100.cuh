@@ -57,7 +57,8 @@
 //             its a_cols x b_cols fp32 outputs at model sizes.
 //
 // The tensor cores' fp32 adds truncate, which biases a long sum: measured
-// 1e-9 of the result per term (2e-6 at 2048 terms, 9e-6 at 8192).  Outputs
+// 1e-9 of the result per term of normal data (2e-6 at 2048 terms, 9e-6 at
+// 8192), up to 7e-9 where all terms have one sign.  Outputs
 // that are kept in fp32 (EPI_OUT_F32) are therefore summed in chunks of
 // kSwChunk k-blocks = 512 terms (5e-7): each chunk has a TMEM accumulator of
 // its own, and the epilogue warps add it, with rounding, to sums in their

@@ -2,7 +2,8 @@
 products grouped by expert (GroupedLinear) and the 8-bit activation
 checkpoints (RowCheckpoint, ActivationCheckpoint).  Each checks its tensors,
 holds its workspace or checkpoint and calls the C ABI; no computation happens
-here, and nothing is recorded for autograd.
+here.  Nothing is recorded for autograd: results are plain tensors, also for
+parameters that require gradients.
 
 Every call runs on ``stream``, or on the current stream of the handle's device
 when none is given; what it allocates (outputs, and at the first call the
@@ -111,7 +112,8 @@ class GroupedLinear(_Handle):
     """One linear layer per expert over ragged row segments.
 
     weight  [G, N, K] (kept alive here, read at every call);
-    rows    rows of x, y, dy and dx;
+    rows    rows of x, y, dy and dx (an upper bound of offsets[G]: a batch of
+            fewer rows uses the first ones);
     bias    [G, N] or None, in the weight's dtype;
     out_dtype  dtype of y and dx (default: the weight's).
 
