@@ -514,7 +514,8 @@ size_t moe_backward_saved_workspace_size(const moe_layer_desc_t* d);
  * descriptor, weights and x.  ckpt is only read.  Errors as moe_backward.
  * bf16: the weight gradients that run on the tensor cores are summed at most
  * 512 terms at a time, as moe_grouped_wgrad's (moe_backward's sums stay whole
- * there: 8e-4 of the value off for 2^17 positive terms). */
+ * there: 8e-4 of the value off for 2^17 positive terms).  Both types: the
+ * bias gradients are summed at most 128 rows at a time. */
 moe_status_t moe_backward_saved(const moe_layer_desc_t* d, const moe_weights_t* w, const void* x,
                                 const void* dy, const void* ckpt, size_t ckpt_bytes,
                                 const moe_grads_t* grads, void* ws, size_t ws_bytes, void* stream);

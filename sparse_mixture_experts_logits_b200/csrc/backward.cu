@@ -245,17 +245,25 @@ __global__ void bwd_pair_kernel(const TY* __restrict__ dy, const float* __restri
   }
 }
 
-// out[g, n] = sum over rows [offsets[g], offsets[g+1]) of Y[row, n], in row order.
+// out[g, n] = sum over rows [offsets[g], offsets[g+1]) of Y[row, n], in row
+// order; chunked: the sum goes to its total every 128 rows, so that a long
+// segment's does not lose the small ones.
 __global__ void bwd_colsum_kernel(const float* __restrict__ Y, long long ldy, const int32_t* __restrict__ offsets,
-                                  long long rows_cap, int N, float* __restrict__ out) {
+                                  long long rows_cap, int N, bool chunked, float* __restrict__ out) {
   const int g = blockIdx.y;
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= N) return;
   const long long b = lmin(max(offsets[g], 0), rows_cap);
   const long long e = lmin(max(offsets[g + 1], 0), rows_cap);
-  float s = 0.f;
-  for (long long r = b; r < e; ++r) s += Y[r * ldy + n];
-  out[static_cast<long long>(g) * N + n] = s;
+  float s = 0.f, t = 0.f;
+  for (long long r = b; r < e; ++r) {
+    s += Y[r * ldy + n];
+    if (chunked && (r - b) % 128 == 127) {
+      t += s;
+      s = 0.f;
+    }
+  }
+  out[static_cast<long long>(g) * N + n] = chunked ? t + s : s;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -430,11 +438,11 @@ cudaError_t launch_bwd_pairs(int dtype, const void* dy, const float* o, const in
 }
 
 cudaError_t launch_bwd_colsum(const float* Y, long long ldy, const int32_t* offsets, int G, long long rows_cap,
-                              int N, float* out, cudaStream_t s) {
+                              int N, bool chunked, float* out, cudaStream_t s) {
   if (G <= 0 || N <= 0) return cudaSuccess;
   if (G > 65535) return cudaErrorInvalidValue;
   dim3 grid((N + 255) / 256, G);
-  bwd_colsum_kernel<<<grid, 256, 0, s>>>(Y, ldy, offsets, rows_cap, N, out);
+  bwd_colsum_kernel<<<grid, 256, 0, s>>>(Y, ldy, offsets, rows_cap, N, chunked, out);
   return cudaGetLastError();
 }
 

@@ -127,40 +127,53 @@ __global__ void dw_finish_kernel(const float* __restrict__ parts, int nparts, co
 }
 
 // out[g, n] = sum over rows [offsets[g], offsets[g+1]) of scale[r] Y[r, n]
-// (scale = 1 when null), bf16 Y, fp32 sums in row order.
+// (scale = 1 when null), bf16 Y, fp32 sums in row order; chunked: a column's
+// sum goes to its total every 128 rows, so that a long segment's does not lose
+// the small ones.
+constexpr int kColsumChunk = 128;
 __global__ void colsum_bf16_kernel(const __nv_bfloat16* __restrict__ Y, long long ldy,
                                    const float* __restrict__ scale, const int32_t* __restrict__ offsets,
-                                   long long rows_cap, int N, float* __restrict__ out) {
+                                   long long rows_cap, int N, bool chunked, float* __restrict__ out) {
   const int g = blockIdx.y;
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= N) return;
   const long long b = min(rows_cap, static_cast<long long>(max(offsets[g], 0)));
   const long long e = min(rows_cap, static_cast<long long>(max(offsets[g + 1], 0)));
-  float s = 0.f;
+  float s = 0.f, t = 0.f;
   for (long long r = b; r < e; ++r) {
     const float v = __bfloat162float(Y[r * ldy + n]);
     s = scale != nullptr ? fmaf(scale[r], v, s) : s + v;
+    if (chunked && (r - b) % kColsumChunk == kColsumChunk - 1) {
+      t += s;
+      s = 0.f;
+    }
   }
-  out[static_cast<long long>(g) * N + n] = s;
+  out[static_cast<long long>(g) * N + n] = chunked ? t + s : s;
 }
 
 // The same sums, two columns per thread (N and ldy even, Y 4-byte aligned):
 // each warp reads 128 contiguous bytes of a row, and the loads of 16 rows are
 // issued before any of them is added, so that a thread keeps 16 requests in
 // flight instead of one.  Each column still adds its rows one by one in row
-// order, so the sums are the scalar kernel's bit for bit.
+// order, so the sums are the scalar kernel's bit for bit (a chunk is a whole
+// number of such turns).
 __global__ void colsum_bf16x2_kernel(const __nv_bfloat162* __restrict__ Y, long long ldy2,
                                      const float* __restrict__ scale, const int32_t* __restrict__ offsets,
-                                     long long rows_cap, int N2, float2* __restrict__ out) {
+                                     long long rows_cap, int N2, bool chunked, float2* __restrict__ out) {
   constexpr int kRows = 16;
   const int g = blockIdx.y;
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= N2) return;
   const long long b = min(rows_cap, static_cast<long long>(max(offsets[g], 0)));
   const long long e = min(rows_cap, static_cast<long long>(max(offsets[g + 1], 0)));
-  float s0 = 0.f, s1 = 0.f;
+  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
   long long r = b;
   for (; r + kRows <= e; r += kRows) {
+    if (chunked && (r - b) % kColsumChunk == 0) {
+      t0 += s0;
+      t1 += s1;
+      s0 = s1 = 0.f;
+    }
     __nv_bfloat162 v[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) v[i] = Y[(r + i) * ldy2 + n];
@@ -188,7 +201,7 @@ __global__ void colsum_bf16x2_kernel(const __nv_bfloat162* __restrict__ Y, long 
       s1 += f.y;
     }
   }
-  out[static_cast<long long>(g) * N2 + n] = make_float2(s0, s1);
+  out[static_cast<long long>(g) * N2 + n] = chunked ? make_float2(t0 + s0, t1 + s1) : make_float2(s0, s1);
 }
 
 // out[g, :] = 0 (per_group floats) for every g with counts[g] == 0.
@@ -253,19 +266,19 @@ cudaError_t launch_dw_finish(const float* parts, int nparts, const int32_t* slot
 }
 
 cudaError_t launch_colsum_bf16(const void* Y, long long ldy, const float* scale, const int32_t* offsets, int G,
-                               long long rows_cap, int N, float* out, cudaStream_t s) {
+                               long long rows_cap, int N, bool chunked, float* out, cudaStream_t s) {
   if (G <= 0 || N <= 0) return cudaSuccess;
   if (G > 65535) return cudaErrorInvalidValue;
   if (N % 2 == 0 && ldy % 2 == 0 && reinterpret_cast<uintptr_t>(Y) % 4 == 0 &&
       reinterpret_cast<uintptr_t>(out) % 8 == 0) {
     dim3 grid((N / 2 + 255) / 256, G);
     colsum_bf16x2_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat162*>(Y), ldy / 2, scale, offsets,
-                                              rows_cap, N / 2, reinterpret_cast<float2*>(out));
+                                              rows_cap, N / 2, chunked, reinterpret_cast<float2*>(out));
     return cudaGetLastError();
   }
   dim3 grid((N + 255) / 256, G);
   colsum_bf16_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(Y), ldy, scale, offsets, rows_cap, N,
-                                          out);
+                                          chunked, out);
   return cudaGetLastError();
 }
 

@@ -185,7 +185,7 @@ cudaError_t launch_zero_pad_rows(const int32_t* counts, const int32_t* offsets_p
 cudaError_t launch_dw_finish(const float* parts, int nparts, const int32_t* slot_pad, const int32_t* idx,
                              const void* dy, const void* b2, int D, int M, int T, int k, float* dw, cudaStream_t s);
 cudaError_t launch_colsum_bf16(const void* Y, long long ldy, const float* scale, const int32_t* offsets, int G,
-                               long long rows_cap, int N, float* out, cudaStream_t s);
+                               long long rows_cap, int N, bool chunked, float* out, cudaStream_t s);
 cudaError_t launch_zero_empty_groups(const int32_t* counts, int G, long long per_group, float* out, cudaStream_t s);
 
 // backward.cu: C (+)= A B^T on the CUDA cores, fp32 sums, with strided
@@ -223,9 +223,9 @@ cudaError_t launch_bwd_act_grad(const float* da, float* h, const int32_t* n_rows
 cudaError_t launch_bwd_pairs(int dtype, const void* dy, const float* o, const int32_t* slot_of,
                              const float* topk_w, float* dw, float* dO, int T, int k, int D, long long rows_cap,
                              cudaStream_t s);
-// out[g, :] = column sums of Y over the rows of group g.
+// out[g, :] = column sums of Y over the rows of group g (chunked: 128 rows at a time).
 cudaError_t launch_bwd_colsum(const float* Y, long long ldy, const int32_t* offsets, int G, long long rows_cap,
-                              int N, float* out, cudaStream_t s);
+                              int N, bool chunked, float* out, cudaStream_t s);
 // dL/dlogits [T, M] from dL/dw [T, k] (fp32), and a bf16 copy when dl_bf is
 // not null (the operand of the router's tensor-core backward GEMMs).
 cudaError_t launch_bwd_router(const float* logits, const int32_t* idx, const float* dw, int T, int M, int k,

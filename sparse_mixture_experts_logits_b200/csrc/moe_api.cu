@@ -1443,7 +1443,7 @@ moe_status_t saved_backward_tc(const moe_layer_desc_t* d, const moe_weights_t* w
     gd.part = at<float*>(ws, L.colsum);
     MOE_CUDA(launch_grouped_tc(gd, at<void*>(ws, L.wgrad), s));
     MOE_CUDA(launch_dw_finish(parts, nparts, slot_of, idx, dy, biases ? w->b2 : nullptr, D, M, T, k, dwp, s));
-    if (biases) MOE_CUDA(launch_colsum_bf16(dyp, D, row_w, offsets, M, pairs, D, g->db2, s));
+    if (biases) MOE_CUDA(launch_colsum_bf16(dyp, D, row_w, offsets, M, pairs, D, true, g->db2, s));
   }
   if (d->I_sh > 0)
     MOE_TRY(shared_backward_tc(d, w, x, dy, g, nullptr, at<int8_t*>(ckpt, C.sq), at<uint8_t*>(ckpt, C.se),
@@ -1578,8 +1578,8 @@ moe_status_t backward_tc_impl(const moe_layer_desc_t* d, const moe_weights_t* w,
     MOE_CUDA(launch_zero_empty_groups(counts, M, 1ll * n1 * D, g->dw1, s));
     MOE_CUDA(launch_dw_finish(parts, nparts, slotp, idx, dy, biases ? w->b2 : nullptr, D, M, T, k, dwp, s));
     if (biases) {
-      MOE_CUDA(launch_colsum_bf16(dypp, D, rwp, offp, M, P, D, g->db2, s));
-      MOE_CUDA(launch_colsum_bf16(dhb, n1, nullptr, offp, M, P, Ha, g->db1, s));
+      MOE_CUDA(launch_colsum_bf16(dypp, D, rwp, offp, M, P, D, false, g->db2, s));
+      MOE_CUDA(launch_colsum_bf16(dhb, n1, nullptr, offp, M, P, Ha, false, g->db1, s));
     }
   }
   MOE_TRY(shared_backward_tc(d, w, x, dy, g, at<void*>(ws, L.hsb), nullptr, nullptr, nullptr,
@@ -1697,8 +1697,8 @@ moe_status_t backward_f32(const moe_layer_desc_t* d, const moe_weights_t* w, con
     g6.mode = 1; g6.offsets = offsets; g6.G = M; g6.c_gstride = 1ll * n1 * D;
     MOE_CUDA(launch_bwd_gemm(g6, s));
     if (biases) {
-      MOE_CUDA(launch_bwd_colsum(dO, D, offsets, M, pairs, D, g->db2, s));
-      MOE_CUDA(launch_bwd_colsum(hpre, n1, offsets, M, pairs, Ha, g->db1, s));
+      MOE_CUDA(launch_bwd_colsum(dO, D, offsets, M, pairs, D, ckpt != nullptr, g->db2, s));
+      MOE_CUDA(launch_bwd_colsum(hpre, n1, offsets, M, pairs, Ha, ckpt != nullptr, g->db1, s));
     }
   }
   if (Is > 0) {

@@ -123,3 +123,21 @@ def test_a_stream_of_its_own(B, name, kept):
     for n, v in want.items():
         assert torch.equal(got[n], v), n
     assert layer.device_status(stream=side) == 0 and layer.backward_status(stream=side) == 0
+
+
+@pytest.mark.parametrize("name", ["glam_small_bf16", "glam_nonorm_f32"])
+def test_bias_gradients_over_many_tokens(B, name):
+    """One large gradient and 10^5 small ones whose last bits the large one's sum
+    does not hold: at most 128 rounded additions in a row, and one for each 128
+    rows behind them.  (One expert, whose gate weight is 1.)"""
+    T = 100_000
+    cfg = ms.get_config(name, T=T, D=16, M=1, k=1, I=16)
+    inp = gpu_inputs(cfg)
+    dy = torch.full_like(inp["x"], 1.0078125)
+    dy[0] = 2.0 ** 17
+    layer = B.MoELayer(cfg, inp)
+    ck = B.LayerCheckpoint(layer)
+    layer.forward(inp["x"], checkpoint=ck)
+    got = layer.backward(inp["x"], dy, checkpoint=ck)
+    assert ck.view("topk_w").eq(1).all()
+    _close(got["db2"][0], dy.double().sum(0), (128 + T / 128 + 2) * 2.0 ** -24, "db2")
